@@ -83,7 +83,7 @@ def draw(rng):
         seqs = min(tokens, _log_int(rng, 1, 300))
         step = rng.random() < 0.4
         if step:  # one token for each sequence
-            seqs = tokens = min(tokens, 700)
+            seqs = tokens = min(tokens, 400)
         return dict(op=op, cache=rng.choice(["bf16", "e4m3", "int4"]), seqs=seqs, tokens=tokens,
                     heads=kv_heads * rng.choice([1, 2, 4, 7, 8]), kv_heads=kv_heads, dim=dim,
                     rotary=rng.choice([dim, dim, dim // 2, 16]), interleaved=rng.random() < 0.5, page=page,
@@ -108,7 +108,7 @@ def _quantize(x):
     g = x.unflatten(-1, (-1, GROUP))
     lo, hi = g.amin(-1), g.amax(-1)
     low = lo.bfloat16()
-    step = (hi / 15 - lo / 15).bfloat16()
+    step = ((hi - lo) / 15).bfloat16()
     bad = ~(torch.isfinite(low) & torch.isfinite(step))
     low, step = low.masked_fill(bad, math.nan), step.masked_fill(bad, math.nan)
     s = step.to(x.dtype).unsqueeze(-1)
