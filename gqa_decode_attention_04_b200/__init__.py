@@ -7,6 +7,8 @@ is missing or the tensors are not on a CUDA device, the calls raise.
 
     kv_append(k_new, v_new, k_pages, v_pages, block_table, positions)
     paged_decode_attn(q, k_pages, v_pages, block_table, seq_lens, out=None, scale=None)
+    rope_kv_append(q, k_new, v_new, cos_sin, k_pages, v_pages, block_table, positions, ...)
+    paged_decode_attn_int4(q, kv_pages, block_table, seq_lens, ...)      4-bit cache
     Pager(num_pages, page_size, max_seqs, max_blocks_per_seq)   host page bookkeeping
 """
 from __future__ import annotations
@@ -32,6 +34,16 @@ __all__ = [
     "kv_append_multi",
     "paged_multi_query_attn",
     "multi_query_step",
+    "rope_kv_append",
+    "rope_kv_append_fp8",
+    "rope_kv_append_int4",
+    "quantize_pages_int4",
+    "dequantize_pages_int4",
+    "kv_append_int4",
+    "int4_workspace",
+    "paged_decode_attn_int4",
+    "paged_multi_query_attn_int4",
+    "decode_step_int4",
     "check_device_error",
     "kv_cache_bytes",
     "set_num_workers",
@@ -78,6 +90,18 @@ EXPORTED_SYMBOLS = (
     "gqa_pager_gather",
     "gqa_pager_free_pages",
     "gqa_pager_seq_len",
+    # include/gqa_rope.h
+    "gqa_rope_kv_append",
+    "gqa_rope_kv_append_fp8",
+    "gqa_rope_kv_append_int4",
+    # include/gqa_int4.h
+    "gqa_kv_quantize_int4",
+    "gqa_kv_dequantize_int4",
+    "gqa_kv_append_int4",
+    "gqa_int4_workspace_bytes",
+    "gqa_paged_decode_attn_int4",
+    "gqa_paged_multi_query_attn_int4",
+    "gqa_decode_step_int4",
 )
 
 
@@ -164,6 +188,27 @@ def load_library() -> ctypes.CDLL:
     lib.gqa_pager_free_pages.restype = i32
     lib.gqa_pager_seq_len.argtypes = [vp, i32]
     lib.gqa_pager_seq_len.restype = i32
+    sz = ctypes.c_size_t
+    lib.gqa_rope_kv_append.argtypes = [vp] * 10 + [i32] * 8 + [i64] * 3 + [i32] * 3 + [vp]
+    lib.gqa_rope_kv_append.restype = i32
+    lib.gqa_rope_kv_append_fp8.argtypes = [vp] * 12 + [i32] * 8 + [i64] * 3 + [i32] * 3 + [vp]
+    lib.gqa_rope_kv_append_fp8.restype = i32
+    lib.gqa_rope_kv_append_int4.argtypes = [vp] * 9 + [i32] * 8 + [i64] * 3 + [i32] * 3 + [vp]
+    lib.gqa_rope_kv_append_int4.restype = i32
+    lib.gqa_kv_quantize_int4.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp]
+    lib.gqa_kv_quantize_int4.restype = i32
+    lib.gqa_kv_dequantize_int4.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp]
+    lib.gqa_kv_dequantize_int4.restype = i32
+    lib.gqa_kv_append_int4.argtypes = [vp] * 5 + [i32] * 6 + [vp]
+    lib.gqa_kv_append_int4.restype = i32
+    lib.gqa_int4_workspace_bytes.argtypes = []
+    lib.gqa_int4_workspace_bytes.restype = sz
+    lib.gqa_paged_decode_attn_int4.argtypes = [vp] * 5 + [i32] * 5 + [f32, i32, i32, vp, sz, vp]
+    lib.gqa_paged_decode_attn_int4.restype = i32
+    lib.gqa_paged_multi_query_attn_int4.argtypes = [vp] * 5 + [i32] * 6 + [f32, i32, i32, vp, sz, vp]
+    lib.gqa_paged_multi_query_attn_int4.restype = i32
+    lib.gqa_decode_step_int4.argtypes = [vp] * 10 + [i32] * 8 + [f32, i32, i32, vp, sz, vp]
+    lib.gqa_decode_step_int4.restype = i32
     _lib = lib
     return lib
 
@@ -510,6 +555,289 @@ def decode_step_fp8(q, k_new, v_new, k_pages, v_pages, k_scales, v_scales, block
             k_scales.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(), positions.data_ptr(),
             seq_lens.data_ptr(), out.data_ptr(), B, H, Hk, D, ps, float(scale), block_table.shape[1], P,
             _stream_ptr(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ rotating appends, 4-bit cache
+class _on:
+    """Makes dev, and the given stream where there is one, current; .ptr is the stream to launch on.
+    What a call allocates itself is made inside, so it belongs to the stream that it is used on."""
+
+    __slots__ = ("ptr", "_guards")
+
+    def __init__(self, dev, stream):
+        self._guards = ()
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=dev)
+            self.ptr = stream.cuda_stream
+            self._guards = (torch.cuda.device(dev), torch.cuda.stream(stream))
+        else:
+            self.ptr = torch.cuda.current_stream(dev).cuda_stream
+            if dev.index != torch.cuda.current_device():
+                self._guards = (torch.cuda.device(dev),)
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+        return False
+
+
+def _need_rows(t, name, shape, dev):
+    """bf16 rows [T, heads, head_dim], contiguous but for the stride between tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be [num_tokens, heads, head_dim]" + (f" = {list(shape)}" if shape else ""))
+    T, h, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if T > 1 else h * d
+
+
+def _rope(fn, q, k_new, v_new, cos_sin, pools, scales, block_table, positions, seq_ids, interleaved, q_out, stream,
+          pool_shape):
+    dev = pools[0].device
+    P, Hk, ps, D = pool_shape
+    q_stride = _need_rows(q, "q", None, dev)
+    T, H, Dq = q.shape
+    if Dq != D:
+        raise ValueError("q's head_dim differs from the pools'")
+    k_stride = _need_rows(k_new, "k_new", (T, Hk, D), dev)
+    v_stride = _need_rows(v_new, "v_new", (T, Hk, D), dev)
+    _need(cos_sin, "cos_sin", torch.float32, dev)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_positions, rotary_dim]")
+    _need(block_table, "block_table", torch.int32, dev)
+    _need(positions, "positions", torch.int32, dev)
+    if block_table.dim() != 2 or tuple(positions.shape) != (T,):
+        raise ValueError("block_table must be [num_seqs, max_blocks], positions [num_tokens]")
+    if seq_ids is not None:
+        _need(seq_ids, "seq_ids", torch.int32, dev)
+        if tuple(seq_ids.shape) != (T,):
+            raise ValueError("seq_ids must be [num_tokens]")
+    elif block_table.shape[0] != T:
+        raise ValueError("without seq_ids, token t is sequence t: block_table must have num_tokens rows")
+    with _on(dev, stream) as ptr:
+        q_out = _multi_out(q_out, (T, H, D), dev)
+        _check(fn(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), cos_sin.data_ptr(), q_out.data_ptr(),
+                  *(t.data_ptr() for t in (*pools, *scales)), block_table.data_ptr(), positions.data_ptr(),
+                  None if seq_ids is None else seq_ids.data_ptr(), T, block_table.shape[0], H, Hk, D, cos_sin.shape[1],
+                  1 if interleaved else 0, cos_sin.shape[0], q_stride, k_stride, v_stride, ps, block_table.shape[1], P,
+                  ptr))
+    return q_out
+
+
+def rope_kv_append(q, k_new, v_new, cos_sin, k_pages, v_pages, block_table, positions,
+                   seq_ids: Optional[torch.Tensor] = None, interleaved: bool = False,
+                   q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotate q [T, H, D] and k_new [T, Hk, D] by their positions and append k and v to the bf16 pools.
+
+    Row t belongs to sequence seq_ids[t] (t when None) at positions[t]; cos_sin [max_positions,
+    rotary_dim] float32 holds the cosines, then the sines, of a position's rotary_dim / 2 angles.
+    Pairs are channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved.  q, k_new and
+    v_new may be views with a stride between tokens (a fused projection).  Returns the rotated q
+    (q_out, which may be q itself when q is contiguous).  Rows with seq_ids[t] < 0 are padding.
+    """
+    dev = k_pages.device
+    _need(k_pages, "k_pages", torch.bfloat16, dev)
+    _need(v_pages, "v_pages", torch.bfloat16, dev)
+    if k_pages.dim() != 4 or tuple(v_pages.shape) != tuple(k_pages.shape):
+        raise ValueError("page pools must both be [num_pages, num_kv_heads, page_size, head_dim]")
+    return _rope(load_library().gqa_rope_kv_append, q, k_new, v_new, cos_sin, (k_pages, v_pages), (), block_table,
+                 positions, seq_ids, interleaved, q_out, stream, k_pages.shape)
+
+
+def rope_kv_append_fp8(q, k_new, v_new, cos_sin, k_pages, v_pages, k_scales, v_scales, block_table, positions,
+                       seq_ids: Optional[torch.Tensor] = None, interleaved: bool = False,
+                       q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """rope_kv_append into e4m3 pools (the fp32 rotated k and v, divided by their scales)."""
+    dev = k_pages.device
+    shape = _pools_fp8(k_pages, v_pages, k_scales, v_scales, dev)
+    return _rope(load_library().gqa_rope_kv_append_fp8, q, k_new, v_new, cos_sin, (k_pages, v_pages),
+                 (k_scales, v_scales), block_table, positions, seq_ids, interleaved, q_out, stream, shape)
+
+
+def _pool_int4(kv_pages, dev):
+    _need(kv_pages, "kv_pages", torch.uint8, dev)
+    if kv_pages.dim() != 4 or kv_pages.shape[3] % 18 != 0:
+        raise ValueError("kv_pages must be [num_pages, num_kv_heads, page_size / 16, 18 * head_dim] uint8")
+    P, Hk, tiles, b = kv_pages.shape
+    return P, Hk, 16 * tiles, b // 18
+
+
+def rope_kv_append_int4(q, k_new, v_new, cos_sin, kv_pages, block_table, positions,
+                        seq_ids: Optional[torch.Tensor] = None, interleaved: bool = False,
+                        q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """rope_kv_append into a 4-bit pool."""
+    shape = _pool_int4(kv_pages, kv_pages.device)
+    return _rope(load_library().gqa_rope_kv_append_int4, q, k_new, v_new, cos_sin, (kv_pages,), (), block_table,
+                 positions, seq_ids, interleaved, q_out, stream, shape)
+
+
+def quantize_pages_int4(k_pages, v_pages, kv_pages: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A pair of bf16 pools as one 4-bit pool [num_pages, num_kv_heads, page_size / 16, 18 * head_dim]
+    (uint8; include/gqa_int4.h gives the format)."""
+    dev = k_pages.device
+    _need(k_pages, "k_pages", torch.bfloat16, dev)
+    _need(v_pages, "v_pages", torch.bfloat16, dev)
+    if k_pages.dim() != 4 or tuple(v_pages.shape) != tuple(k_pages.shape):
+        raise ValueError("page pools must both be [num_pages, num_kv_heads, page_size, head_dim]")
+    P, Hk, ps, D = k_pages.shape
+    with _on(dev, stream) as ptr:
+        if kv_pages is None:
+            kv_pages = torch.empty((P, Hk, ps // 16, 18 * D), dtype=torch.uint8, device=dev)
+        else:
+            _need(kv_pages, "kv_pages", torch.uint8, dev)
+            if tuple(kv_pages.shape) != (P, Hk, ps // 16, 18 * D):
+                raise ValueError(f"kv_pages must be {[P, Hk, ps // 16, 18 * D]}")
+        _check(load_library().gqa_kv_quantize_int4(k_pages.data_ptr(), v_pages.data_ptr(), kv_pages.data_ptr(), P, Hk,
+                                                   ps, D, ptr))
+    return kv_pages
+
+
+def dequantize_pages_int4(kv_pages, k_pages: Optional[torch.Tensor] = None, v_pages: Optional[torch.Tensor] = None,
+                          stream=None):
+    """The cached values of a 4-bit pool, rounded to bf16: (k_pages, v_pages)."""
+    dev = kv_pages.device
+    P, Hk, ps, D = shape = _pool_int4(kv_pages, dev)
+    with _on(dev, stream) as ptr:
+        k_pages, v_pages = _multi_out(k_pages, shape, dev), _multi_out(v_pages, shape, dev)
+        _check(load_library().gqa_kv_dequantize_int4(kv_pages.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), P,
+                                                     Hk, ps, D, ptr))
+    return k_pages, v_pages
+
+
+def kv_append_int4(k_new, v_new, kv_pages, block_table, positions, stream=None) -> None:
+    """Write k_new/v_new [B, Hk, D] (bf16) into the 4-bit pool at positions[b]."""
+    dev = kv_pages.device
+    P, Hk, ps, D = _pool_int4(kv_pages, dev)
+    for t, n, dt in ((k_new, "k_new", torch.bfloat16), (v_new, "v_new", torch.bfloat16),
+                     (block_table, "block_table", torch.int32), (positions, "positions", torch.int32)):
+        _need(t, n, dt, dev)
+    B = k_new.shape[0]
+    if tuple(k_new.shape) != (B, Hk, D) or tuple(v_new.shape) != (B, Hk, D):
+        raise ValueError("k_new / v_new must be [num_seqs, num_kv_heads, head_dim]")
+    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(positions.shape) != (B,):
+        raise ValueError("block_table must be [num_seqs, max_blocks], positions [num_seqs]")
+    with _on(dev, stream) as ptr:
+        _check(load_library().gqa_kv_append_int4(k_new.data_ptr(), v_new.data_ptr(), kv_pages.data_ptr(),
+                                                 block_table.data_ptr(), positions.data_ptr(), B, Hk, D, ps,
+                                                 block_table.shape[1], P, ptr))
+
+
+def int4_workspace(device=None) -> torch.Tensor:
+    """A zeroed workspace for the attention calls over a 4-bit cache: one per stream, or per captured
+    graph, whose calls may overlap with others'.  It serves calls of every shape."""
+    return torch.zeros(load_library().gqa_int4_workspace_bytes(), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+# Bytes at the head of a workspace that have to be zero before its first use.
+_WORKSPACE_HEAD = 16384
+
+
+def _workspace(workspace, dev):
+    if workspace is None:  # one of this call's own, on its stream: safe whatever runs beside it
+        workspace = torch.empty(load_library().gqa_int4_workspace_bytes(), dtype=torch.uint8, device=dev)
+        workspace[:_WORKSPACE_HEAD].zero_()
+    _need(workspace, "workspace", torch.uint8, dev)
+    return workspace
+
+
+def _attend_int4(q, kv_pages, block_table, seq_lens, out, scale, workspace, stream, multi):
+    dev = q.device
+    _need(q, "q", torch.bfloat16, dev)
+    P, Hk, ps, D = _pool_int4(kv_pages, dev)
+    _need(block_table, "block_table", torch.int32, dev)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    if q.dim() != (4 if multi else 3) or q.shape[-1] != D:
+        raise ValueError("q must be [num_seqs, %snum_heads, head_dim] with the pool's head_dim" % ("q_len, " if multi else ""))
+    B, H = q.shape[0], q.shape[-2]
+    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(seq_lens.shape) != (B,):
+        raise ValueError("block_table must be [num_seqs, max_blocks], seq_lens [num_seqs]")
+    if scale is None:
+        scale = 1.0 / (D ** 0.5)
+    lib = load_library()
+    with _on(dev, stream) as ptr:
+        out = _multi_out(out, q.shape, dev)
+        ws = _workspace(workspace, dev)
+        fn = lib.gqa_paged_multi_query_attn_int4 if multi else lib.gqa_paged_decode_attn_int4
+        _check(fn(q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), B,
+                  *((q.shape[1],) if multi else ()), H, Hk, D, ps, float(scale), block_table.shape[1], P,
+                  ws.data_ptr(), ws.numel(), ptr))
+    return out
+
+
+def paged_decode_attn_int4(q, kv_pages, block_table, seq_lens, out: Optional[torch.Tensor] = None,
+                           scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """paged_decode_attn over a 4-bit pool.  workspace: int4_workspace() (None: the call makes one)."""
+    return _attend_int4(q, kv_pages, block_table, seq_lens, out, scale, workspace, stream, False)
+
+
+def paged_multi_query_attn_int4(q, kv_pages, block_table, seq_lens, out: Optional[torch.Tensor] = None,
+                                scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                                stream=None) -> torch.Tensor:
+    """paged_multi_query_attn over a 4-bit pool: q, out [B, Q, H, D]."""
+    return _attend_int4(q, kv_pages, block_table, seq_lens, out, scale, workspace, stream, True)
+
+
+def decode_step_int4(q, k_new, v_new, kv_pages, block_table, positions, seq_lens,
+                     cos_sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+                     q_rot: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """One decode step over a 4-bit cache: append k_new/v_new at positions, attend over seq_lens tokens.
+
+    With cos_sin (as rope_kv_append), q and k_new are rotated on the way; q_rot, if given, receives
+    the rotated q.
+    """
+    dev = q.device
+    P, Hk, ps, D = _pool_int4(kv_pages, dev)
+    for t, n, dt in ((q, "q", torch.bfloat16), (k_new, "k_new", torch.bfloat16), (v_new, "v_new", torch.bfloat16),
+                     (block_table, "block_table", torch.int32), (positions, "positions", torch.int32),
+                     (seq_lens, "seq_lens", torch.int32)):
+        _need(t, n, dt, dev)
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError("q must be [num_seqs, num_heads, head_dim] with the pool's head_dim")
+    B, H = q.shape[0], q.shape[1]
+    if tuple(k_new.shape) != (B, Hk, D) or tuple(v_new.shape) != (B, Hk, D):
+        raise ValueError("k_new / v_new must be [num_seqs, num_kv_heads, head_dim]")
+    if (block_table.dim() != 2 or block_table.shape[0] != B or tuple(seq_lens.shape) != (B,)
+            or tuple(positions.shape) != (B,)):
+        raise ValueError("block_table must be [num_seqs, max_blocks]; seq_lens, positions [num_seqs]")
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32, dev)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_positions, rotary_dim]")
+    elif q_rot is not None:
+        raise ValueError("q_rot is given, but no cos_sin")
+    if scale is None:
+        scale = 1.0 / (D ** 0.5)
+    with _on(dev, stream) as ptr:
+        out = _multi_out(out, (B, H, D), dev)
+        if cos_sin is not None:
+            q_rot = _multi_out(q_rot, (B, H, D), dev)
+        ws = _workspace(workspace, dev)
+        _check(load_library().gqa_decode_step_int4(
+            q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), None if cos_sin is None else cos_sin.data_ptr(),
+            None if cos_sin is None else q_rot.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(),
+            positions.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), B, H, Hk, D,
+            0 if cos_sin is None else cos_sin.shape[1], 1 if interleaved else 0,
+            0 if cos_sin is None else cos_sin.shape[0], ps, float(scale), block_table.shape[1], P, ws.data_ptr(),
+            ws.numel(), ptr))
     return out
 
 

@@ -129,6 +129,26 @@ gqa_status ensure_workspace(DeviceState& s, size_t counters, size_t part_o_float
   return GQA_OK;
 }
 
+}  // namespace
+
+gqa_status gqa::host_device(uint32_t** err, int* sms) {
+  DeviceState* st;
+  int dev;
+  gqa_status s = get_state(&st, &dev);
+  if (s != GQA_OK) return s;
+  *err = st->err;
+  *sms = st->sms;
+  return GQA_OK;
+}
+
+gqa::Knobs gqa::host_knobs() {
+  return {g_num_workers.load(), static_cast<uint64_t>(g_wait_limit_ns.load()), g_arm_without_copy.load()};
+}
+
+void gqa::host_count_launches(int n) { g_launches.fetch_add(n); }
+
+namespace {
+
 // ------------------------------------------------------------------ tensor maps
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,

@@ -111,6 +111,77 @@ struct AppendFp8Params {
   int num_seqs, num_kv_heads, groups_per_row, page_size, max_blocks, num_pages;
 };
 
+// Rotate q and k and append k, v (rope_append.cu).
+enum : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheInt4 = 2 };
+struct RopeAppendParams {
+  const uint16_t* q;          // token rows of [H, D], q_stride elements apart; likewise k, v
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* q_out;            // [T, H, D]
+  int64_t q_stride, k_stride, v_stride;
+  const float* cos_sin;       // [max_positions, rotary_dim]
+  const int32_t* block_table; // [num_seqs, max_blocks]
+  const int32_t* positions;   // [T]
+  const int32_t* seq_ids;     // [T], or nullptr: row t is sequence t
+  uint8_t* k_pages;           // the pools; a 4-bit cache has one, in k_pages
+  uint8_t* v_pages;
+  const float* k_scales;      // e4m3 only
+  const float* v_scales;
+  uint32_t* err;
+  int num_tokens, num_seqs, num_heads, num_kv_heads;
+  int rotary_dim;             // 0: nothing is rotated
+  int interleaved, max_positions, page_size, max_blocks, num_pages;
+  int chunks;                 // blocks per token (set by the launcher)
+};
+cudaError_t launch_rope_append(const RopeAppendParams& p, int cache, int head_dim, int sms, cudaStream_t stream);
+
+// A bf16 pool pair to and from the 4-bit pool, by tiles of 16 tokens (kv_int4.cu).
+cudaError_t launch_kv_quantize_int4(const void* k, const void* v, void* tiles, int64_t num_tiles, int head_dim,
+                                    cudaStream_t stream);
+cudaError_t launch_kv_dequantize_int4(const void* tiles, void* k, void* v, int64_t num_tiles, int head_dim,
+                                      cudaStream_t stream);
+
+// Attention over the 4-bit pool (decode_int4.cu).
+struct Int4DecodeParams {
+  const uint16_t* q;          // [B, q_len, H, D] bf16
+  uint16_t* out;
+  const uint8_t* pool;        // [P, Hk, ps / 16, 18 D]
+  const int32_t* block_table; // [B, MB]
+  const int32_t* seq_lens;    // [B]
+  int32_t* counters;          // [kInt4MaxCtas], zero between launches
+  float* slots;               // two per CTA: [rows][D] sums, then [rows][2] (reference, sum)
+  uint32_t* err;
+  int num_seqs, num_heads, num_kv_heads, group, q_len;
+  int rows;                   // query rows per kv head: group * q_len
+  int n_rt;                   // row tiles (segments) per kv head
+  int page_size, tiles_per_page, max_blocks, num_pages;
+  float scale_log2;           // scale * log2(e)
+  uint64_t wait_limit_ns;
+  int arm_without_copy;
+  uint32_t tpp_magic;         // division by tiles_per_page (divisor_magic); 0: by 1
+  int tpp_shift;
+};
+constexpr int kInt4MaxCtas = 4096;
+struct Int4Plan {
+  int n_tiles;        // 8-row MMA tiles of a warp
+  int ctas_per_sm;
+  size_t smem_bytes;
+  size_t slot_bytes;  // of one CTA (two slots)
+};
+Int4Plan plan_decode_int4(int head_dim, int rows);
+cudaError_t launch_decode_int4(const Int4DecodeParams& p, const Int4Plan& plan, int head_dim, int grid,
+                               cudaStream_t stream, bool overlap_previous);
+
+// The library's state that the other host files need (gqa_decode.cu).
+gqa_status host_device(uint32_t** err, int* sms);  // the current device's error word and SMs
+struct Knobs {
+  int workers;
+  uint64_t wait_limit_ns;
+  int arm_without_copy;
+};
+Knobs host_knobs();
+void host_count_launches(int n);
+
 // Launchers (return the cudaError_t of the launch).
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append_fp8(const AppendFp8Params& p, cudaStream_t stream);

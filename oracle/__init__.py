@@ -31,3 +31,14 @@ from .fp8_cache import (  # noqa: F401
     quantize_bf16_pages,
     kv_append_fp8,
 )
+from .int4_cache import (  # noqa: F401
+    int4_quantize_rows,
+    int4_dequantize_rows,
+    int4_write_token,
+    int4_read_token,
+    int4_pool_from_rows,
+    int4_rows_from_pool,
+    rotate_rows_f32,
+    f32_to_bf16_bits,
+    paged_multi_query_attention_int4,
+)
