@@ -36,6 +36,8 @@
 // Safety: every wait is bounded; a warp whose wait runs out sets the error word, treats the rest
 // of its range as masked, drains its own copies (bounded) and still takes part in the merges, so
 // no counter is left behind.  Page ids and lengths are range-checked before use.
+#include <type_traits>
+
 #include "int4_codec.cuh"
 #include "internal.cuh"
 #include "ptx.cuh"
@@ -52,10 +54,11 @@ struct Cfg {
   static constexpr int kRows = 8 * NT;              // query rows of a segment
   static constexpr int kGroups = D / 64;
   static constexpr int kTileBytes = 18 * D;
-  static constexpr int kStages = NT == 1 ? (D == 128 ? 4 : 8) : (D == 128 ? 8 : 12);
+  static constexpr int kUnitBytes = 2 * kTileBytes;
+  static constexpr int kStages = NT == 1 ? 2 : 4;
   static constexpr int kCtas = NT == 1 ? 2 : 1;     // per SM
   static constexpr int kRecFloats = kRows * (D + 2);  // a piece: [rows][D], then (reference, sum)
-  static constexpr int kRingBytes = kStages * kTileBytes;
+  static constexpr int kRingBytes = kStages * kUnitBytes;
   static_assert(kRingBytes >= kRecFloats * 4, "the last piece of a warp is left in its ring");
   static constexpr int kRecBytes = (kRecFloats * 4 + 127) / 128 * 128;
   static constexpr int kSmem = kWarps * (kRingBytes + kRecBytes);
@@ -63,12 +66,14 @@ struct Cfg {
 
 // A piece that a warp's range cut off.
 struct Piece {
-  int64_t start;  // position of the segment's first tile in the list
-  int tiles;      // of the segment; 0: no piece
+  int64_t start;  // position of the segment's first unit in the list
+  int units;      // of the segment; 0: no piece
   int b, seg;     // sequence and segment in it
 };
 
-__device__ __forceinline__ int tiles_of(int len) { return (len + int4::kTile - 1) / int4::kTile; }
+constexpr int kUnit = 2 * int4::kTile;  // tokens per step of a warp
+
+__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
 
 // The length of sequence b, 0 if it is out of range.
 __device__ __forceinline__ int checked_len(const Int4DecodeParams& p, int b) {
@@ -130,10 +135,10 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
 
   if (lane == 0) {
 #pragma unroll
-    for (int s = 0; s < C::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&full[warp][s]), 1);
+    for (int s = 0; s < C::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&full[warp][s]), 2);  // lanes 0 and 1
     ptx::fence_mbarrier_init();
-    pieces[2 * warp].tiles = 0;
-    pieces[2 * warp + 1].tiles = 0;
+    pieces[2 * warp].units = 0;
+    pieces[2 * warp + 1].units = 0;
   }
 
   // ---- the split: tiles before each thread's chunk of sequences
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   {
     int64_t mine = 0;
     const int b0 = threadIdx.x * chunk, b1 = min(p.num_seqs, b0 + chunk);
-    for (int b = b0; b < b1; ++b) mine += tiles_of(checked_len(p, b));
+    for (int b = b0; b < b1; ++b) mine += units_of(checked_len(p, b));
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -191,7 +196,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     int len = 0;
     for (;; b += 32) {
       const int mine = b + lane < p.num_seqs ? checked_len(p, b + lane) : 0;
-      int64_t incl = tiles_of(mine);
+      int64_t incl = units_of(mine);
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
@@ -202,58 +207,63 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
         const int at = __ffs(past) - 1;
         b += at;
         len = __shfl_sync(0xffffffffu, mine, at);
-        base += __shfl_sync(0xffffffffu, incl, at) - tiles_of(len);
+        base += __shfl_sync(0xffffffffu, incl, at) - units_of(len);
         break;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
       if (b + 32 >= p.num_seqs) break;  // only if the lengths changed under the call
     }
     if (len == 0) pos = end;
-    int seg = static_cast<int>((pos - base * segs) / max(1, tiles_of(len)));
-    int tile = static_cast<int>(pos - base * segs - static_cast<int64_t>(seg) * tiles_of(len));
+    int seg = static_cast<int>((pos - base * segs) / max(1, units_of(len)));
+    int unit0 = static_cast<int>(pos - base * segs - static_cast<int64_t>(seg) * units_of(len));
+    int left = static_cast<int>(min(end - pos, int64_t{INT32_MAX}));  // units to do
 
-    // ---- the copies' cursor runs kStages tiles ahead of the arithmetic's
-    int pb = b, phead = seg / p.n_rt, prt = seg - phead * p.n_rt, ptile = tile, plen = len;
-    int64_t ppos = pos;
-    int win = -1;         // first block of the block-table window (32 entries, one per lane)
-    int win_b = -1;
-    int entry = 0;
-    uint32_t bad = 0, phase = 0;  // bit per stage: no data behind this tile; parity to wait for
-    int pstage = 0;
+    // ---- the copies' cursor runs kStages units ahead of the arithmetic's.  Lanes 0 and 1 bring
+    // one tile each of a unit.
+    int pb = b, phead = seg / p.n_rt, prt = seg - phead * p.n_rt, punit = unit0, plen = len, pleft = left;
+    int win = -1, win_b = -1;  // first block and sequence of the block-table window (one entry per lane)
+    int entry = 0, pstage = 0;
+    uint32_t bad = 0, phase = 0;  // two bits per stage: no data behind the tile; bit per stage: parity to wait for
+    const uint32_t ring_at = ptx::smem_u32(ring), bar_at = ptx::smem_u32(&full[warp][0]);
     auto produce = [&]() {
-      if (ppos >= end) return;
+      if (pleft <= 0) return;
+      const int ptile = 2 * punit + (lane & 1);
       const int block = p.tpp_magic != 0 ? fast_div(ptile, p.tpp_magic, p.tpp_shift) : ptile;
-      if (pb != win_b || block < win || block >= win + 32) {
-        win = block;
+      const int block0 = p.tpp_magic != 0 ? fast_div(2 * punit, p.tpp_magic, p.tpp_shift) : 2 * punit;
+      // (31: the unit's second tile may be in the next block)
+      if (pb != win_b || static_cast<unsigned>(block0 - win) >= 31u) {
+        win = block0;
         win_b = pb;
         entry = win + lane < p.max_blocks ? __ldg(p.block_table + static_cast<int64_t>(pb) * p.max_blocks + win + lane) : -1;
       }
       const int page = __shfl_sync(0xffffffffu, entry, block - win);
-      const uint32_t bar = ptx::smem_u32(&full[warp][pstage]);
-      if (page >= 0 && page < p.num_pages) {
-        bad &= ~(1u << pstage);
-        if (lane == 0) {
-          const int64_t at = (static_cast<int64_t>(page) * p.num_kv_heads + phead) * p.tiles_per_page + (ptile - block * p.tiles_per_page);
+      const bool wanted = ptile * int4::kTile < plen;  // (the last unit may be one tile)
+      const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
+      const unsigned lost = __ballot_sync(0xffffffffu, !ok || !wanted) & 3u;
+      bad = (bad & ~(3u << (2 * pstage))) | (lost << (2 * pstage));
+      if (lane < 2) {
+        const uint32_t bar = bar_at + 8 * pstage;
+        if (ok && wanted) {
+          const uint32_t at = (static_cast<uint32_t>(page) * p.num_kv_heads + phead) * p.tiles_per_page +
+                              (ptile - block * p.tiles_per_page);
           ptx::mbar_arrive_expect_tx(bar, C::kTileBytes);
           if (!p.arm_without_copy)
-            ptx::bulk_load(ptx::smem_u32(ring + pstage * C::kTileBytes), p.pool + at * C::kTileBytes, C::kTileBytes, bar);
-        }
-      } else {
-        bad |= 1u << pstage;
-        if (lane == 0) {
-          atomicOr(p.err, kErrBounds);
+            ptx::bulk_load(ring_at + pstage * C::kUnitBytes + lane * C::kTileBytes,
+                           p.pool + static_cast<uint64_t>(at) * C::kTileBytes, C::kTileBytes, bar);
+        } else {
+          if (wanted) atomicOr(p.err, kErrBounds);
           ptx::mbar_arrive(bar);
         }
       }
       pstage = pstage + 1 == C::kStages ? 0 : pstage + 1;
-      ++ppos;
-      if (++ptile == tiles_of(plen)) {
-        ptile = 0;
+      --pleft;
+      if (++punit == units_of(plen)) {
+        punit = 0;
         if (++prt == p.n_rt) {
           prt = 0;
           if (++phead == p.num_kv_heads) {
             phead = 0;
-            if (ppos < end) plen = next_len(p, pb);
+            if (pleft > 0) plen = next_len(p, pb);
           }
         }
       }
@@ -263,16 +273,16 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
 
     int stage = 0;
     bool dead = false;
-    while (pos < end) {
-      // ---- a piece: tiles [tile, tile + count) of segment (b, seg)
-      const int n = tiles_of(len);
-      const int count = static_cast<int>(min(static_cast<int64_t>(n - tile), end - pos));
+    while (left > 0) {
+      // ---- a piece: units [unit0, unit0 + count) of segment (b, seg)
+      const int n = units_of(len);
+      const int count = min(n - unit0, left);
       const int head = seg / p.n_rt, row0 = (seg - head * p.n_rt) * C::kRows;
 
       // q fragments (B operand: k = channels, n = rows), row sums and scales
       uint32_t qf[NT][2 * G * 2][2];
-      float h[NT][2], qs[NT][G][2];
-      int lim[NT][2];  // tokens that the row sees
+      uint32_t qsum[NT];  // B operand of the minima's product: k = t holds group t % G, its upper then lower bits
+      float h[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = row0 + nt * 8 + g;
@@ -320,17 +330,18 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           qf[nt][2 * i + 1][0] = ptx::pack_f16x2(y[2] * up, y[6] * up);
           qf[nt][2 * i + 1][1] = ptx::pack_f16x2(y[3] * up4, y[7] * up4);
         }
+        // The sum of q in the units of the codes' products, cut into two parts of 11 bits, which
+        // tf32 holds exactly: the minima (bf16) times them lose 2^-22 at most.
+        const float mine = (G == 2 && (t & 1) ? sum[G - 1] : sum[0]) * up * 0x1p-24f;
+        const float upper = __uint_as_float(__float_as_uint(mine) & 0xffffe000u);
+        const float lower = __uint_as_float(__float_as_uint(mine - upper) & 0xffffe000u);
+        qsum[nt] = __float_as_uint(t / G == 0 ? upper : (t / G == 1 ? lower : 0.0f));
         // this thread's score columns are rows 2 t and 2 t + 1 of the row tile
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          h[nt][c] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * c);
-#pragma unroll
-          for (int u = 0; u < G; ++u) qs[nt][u][c] = p.scale_log2 * __shfl_sync(0xffffffffu, sum[u], 8 * t + 4 * c);
-          lim[nt][c] = min(len, len - p.q_len + 1 + token_of(p, row0 + nt * 8 + 2 * t + c));
-        }
+        for (int c = 0; c < 2; ++c) h[nt][c] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * c);
       }
 
-      float o[G * 4][NT][4], l[NT][2], pm[NT][G][2], ref[NT][2], F[NT][G][2];
+      float o[G * 4][NT][4], l[NT][2], pm[NT][G][2], ref[NT][2], F[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -341,212 +352,249 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
         for (int c = 0; c < 2; ++c) {
           l[nt][c] = 0.0f;
           ref[nt][c] = kNone;
+          F[nt][c] = 1.0f;
 #pragma unroll
-          for (int u = 0; u < G; ++u) {
-            pm[nt][u][c] = 0.0f;
-            F[nt][u][c] = 1.0f;
-          }
+          for (int u = 0; u < G; ++u) pm[nt][u][c] = 0.0f;
         }
       }
 
+      // One tile whose first token is tok0.  ENDS: some row's window ends in it.
+      auto attend = [&](const unsigned char* at, int tok0, auto ends_tag) {
+        constexpr bool ENDS = decltype(ends_tag)::value;
+        // ---- S^T = K Q^T per group, and the minima's part of it
+        float s[NT][G][4], bias[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            bias[nt][x] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < G; ++u) s[nt][u][x] = 0.0f;
+          }
+        uint32_t ka[2 * G], kb[2 * G];
+        uint32_t par[2][2 * G];  // tokens g, g + 8: (step, low) of K's groups, then V's
+        if (G == 2) {
+          const uint4 a = *reinterpret_cast<const uint4*>(at + g * 64 + t * 16);
+          const uint4 c = *reinterpret_cast<const uint4*>(at + (g + 8) * 64 + t * 16);
+          ka[0] = a.x; ka[1] = a.y; ka[2 * G - 2] = a.z; ka[2 * G - 1] = a.w;
+          kb[0] = c.x; kb[1] = c.y; kb[2 * G - 2] = c.z; kb[2 * G - 1] = c.w;
+          const uint4 pa = *reinterpret_cast<const uint4*>(at + L4::kParams + g * 16);
+          const uint4 pc = *reinterpret_cast<const uint4*>(at + L4::kParams + (g + 8) * 16);
+          par[0][0] = pa.x; par[0][1] = pa.y; par[0][2 * G - 2] = pa.z; par[0][2 * G - 1] = pa.w;
+          par[1][0] = pc.x; par[1][1] = pc.y; par[1][2 * G - 2] = pc.z; par[1][2 * G - 1] = pc.w;
+        } else {
+          const uint2 a = *reinterpret_cast<const uint2*>(at + g * 32 + t * 8);
+          const uint2 c = *reinterpret_cast<const uint2*>(at + (g + 8) * 32 + t * 8);
+          ka[0] = a.x; ka[1] = a.y;
+          kb[0] = c.x; kb[1] = c.y;
+          const uint2 pa = *reinterpret_cast<const uint2*>(at + L4::kParams + g * 8);
+          const uint2 pc = *reinterpret_cast<const uint2*>(at + L4::kParams + (g + 8) * 8);
+          par[0][0] = pa.x; par[0][1] = pa.y;
+          par[1][0] = pc.x; par[1][1] = pc.y;
+        }
+        {
+          const uint32_t low_a = (G == 2 && (t & 1) ? par[0][G - 1] : par[0][0]) & 0xffff0000u;
+          const uint32_t low_c = (G == 2 && (t & 1) ? par[1][G - 1] : par[1][0]) & 0xffff0000u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) ptx::mma_tf32_1684(bias[nt], low_a, low_c, qsum[nt]);
+        }
+#pragma unroll
+        for (int w = 0; w < 2 * G; ++w) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t a = half ? ka[w] >> 8 : ka[w], c = half ? kb[w] >> 8 : kb[w];
+            const uint32_t frag[4] = {a & kLo, c & kLo, a & kHi, c & kHi};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              ptx::mma_f16_16816(s[nt][w / 2], frag, qf[nt][2 * w + half][0], qf[nt][2 * w + half][1]);
+          }
+        }
+        float step[2][G], low[2][G];  // of V: [token g, g + 8][group]
+        float sc[NT][4];              // scores, in units of log2 once multiplied by h
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int u = 0; u < G; ++u) {
+            step[r][u] = __uint_as_float(par[r][G + u] << 16);
+            low[r][u] = __uint_as_float(par[r][G + u] & 0xffff0000u);
+            const float ks = __uint_as_float(par[r][u] << 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                sc[nt][2 * r + c] = fmaf(ks, s[nt][u][2 * r + c], u == 0 ? bias[nt][2 * r + c] : sc[nt][2 * r + c]);
+          }
+          if (ENDS && tok0 + g + 8 * r >= len) {  // past the sequence: no parameters
+#pragma unroll
+            for (int u = 0; u < G; ++u) step[r][u] = low[r][u] = 0.0f;
+          }
+        }
+        bool seen[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            seen[nt][x] = true;
+            if (ENDS) {
+              const int lim = min(len, len - p.q_len + 1 + token_of(p, row0 + nt * 8 + 2 * t + x % 2));
+              seen[nt][x] = tok0 + g + 8 * (x / 2) < lim;
+            }
+          }
+        // ---- weights; the reference moves only when a score passes it by 2^8
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint64_t hh = ptx::f2_pack(h[nt][0], h[nt][1]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint64_t y = ptx::f2_mul(ptx::f2_pack(sc[nt][2 * r], sc[nt][2 * r + 1]), hh);
+            ptx::f2_unpack(y, sc[nt][2 * r], sc[nt][2 * r + 1]);
+          }
+        }
+        float pr[NT][4], w[NT][G][4];
+        bool up;
+        auto weigh = [&]() {
+          float big = 0.0f, top = 0.0f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              // (packed pairs: the two rows of a token)
+              float y[2];
+              ptx::f2_unpack(ptx::f2_sub(ptx::f2_pack(sc[nt][2 * r], sc[nt][2 * r + 1]), ptx::f2_pack(ref[nt][0], ref[nt][1])), y[0], y[1]);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                pr[nt][2 * r + c] = ptx::ex2(y[c]);
+                if (ENDS && !seen[nt][2 * r + c]) pr[nt][2 * r + c] = 0.0f;
+              }
+              ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(pr[nt][2 * r], pr[nt][2 * r + 1]), ptx::f2_pack(F[nt][0], F[nt][1])), y[0], y[1]);
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int u = 0; u < G; ++u) {
+                  w[nt][u][2 * r + c] = y[c] * step[r][u];
+                  if (ENDS && !seen[nt][2 * r + c]) w[nt][u][2 * r + c] = 0.0f;
+                }
+            }
+            top = ptx::max3(top, pr[nt][0], pr[nt][1]);
+            top = ptx::max3(top, pr[nt][2], pr[nt][3]);
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+              big = ptx::max3(big, w[nt][u][0], w[nt][u][1]);
+              big = ptx::max3(big, w[nt][u][2], w[nt][u][3]);
+            }
+          }
+          up = top > 256.0f || big > 32768.0f;
+        };
+        weigh();
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float top = ref[nt][c], at0 = sc[nt][c], at1 = sc[nt][c + 2];
+              if (seen[nt][c]) top = fmaxf(top, at0);
+              if (seen[nt][c + 2]) top = fmaxf(top, at1);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              const float a = ptx::ex2(ref[nt][c] - top);
+              ref[nt][c] = top;
+              l[nt][c] *= a;
+              float big = 0.0f;
+#pragma unroll
+              for (int u = 0; u < G; ++u) {
+                pm[nt][u][c] *= a;
+                if (seen[nt][c]) big = fmaxf(big, ptx::ex2(at0 - top) * step[0][u]);
+                if (seen[nt][c + 2]) big = fmaxf(big, ptx::ex2(at1 - top) * step[1][u]);
+              }
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+              // the largest weight so far in [2^6, 2^8): 2^8 below the bound, as far as scores may pass
+              // the reference, and 2^20 above fp16's subnormals
+              const float before = a / F[nt][c];
+              const float f = inverse_pow2(fmaxf(big * 0x1p-6f, before));
+              const float scale = before * f;
+              F[nt][c] = f;
+#pragma unroll
+              for (int m = 0; m < 4 * G; ++m) {
+                o[m][nt][c] *= scale;
+                o[m][nt][c + 2] *= scale;
+              }
+            }
+          weigh();
+        }
+        uint32_t pb16[NT][G][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(l[nt][0], l[nt][1]), ptx::f2_pack(pr[nt][2 * r], pr[nt][2 * r + 1])), l[nt][0], l[nt][1]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+              if (!ENDS || seen[nt][x]) pm[nt][u][x % 2] = fmaf(pr[nt][x], low[x / 2][u], pm[nt][u][x % 2]);
+          }
+#pragma unroll
+          for (int u = 0; u < G; ++u) {
+            pb16[nt][u][0] = ptx::movmatrix_trans(ptx::pack_f16x2(w[nt][u][0], w[nt][u][1]));
+            pb16[nt][u][1] = ptx::movmatrix_trans(ptx::pack_f16x2(w[nt][u][2], w[nt][u][3]));
+          }
+        }
+        // ---- O^T += V^T P^T: tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of this thread's channels
+        uint32_t v[4][G];
+        const unsigned char* vat = at + L4::kVCodes + (g / (8 / G)) * 512 + t * 32 + (g % (8 / G)) * (4 * G);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (G == 2) {
+            const uint2 a = *reinterpret_cast<const uint2*>(vat + q * 128);
+            v[q][0] = a.x;
+            v[q][G - 1] = a.y;
+          } else {
+            v[q][0] = *reinterpret_cast<const uint32_t*>(vat + q * 128);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t sel = m < 2 ? 0x5410u : 0x7632u;
+            uint32_t a = prmt(v[0][u], v[1][u], sel), c = prmt(v[2][u], v[3][u], sel);
+            if (m % 2) {
+              a >>= 8;
+              c >>= 8;
+            }
+            const uint32_t frag[4] = {a & kLo, a & kHi, c & kLo, c & kHi};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) ptx::mma_f16_16816(o[4 * u + m][nt], frag, pb16[nt][u][0], pb16[nt][u][1]);
+          }
+      };
+
       for (int i = 0; i < count; ++i) {
-        const uint32_t bar = ptx::smem_u32(&full[warp][stage]);
         if (!dead) {
-          const bool ok = ptx::mbar_wait_bounded(bar, (phase >> stage) & 1u, p.wait_limit_ns);
+          const bool ok = ptx::mbar_wait_bounded(bar_at + 8 * stage, (phase >> stage) & 1u, p.wait_limit_ns);
           if (!__all_sync(0xffffffffu, ok)) {
             dead = true;
             if (lane == 0) atomicOr(p.err, kErrTimeout);
             if (!p.arm_without_copy) {  // nothing may still be landing when the ring is written or given up
-              const int in_flight = static_cast<int>(ppos - pos) - i;
+              const int in_flight = left - pleft - i;
               for (int k = 0, st = stage; k < in_flight; ++k, st = st + 1 == C::kStages ? 0 : st + 1)
-                ptx::mbar_wait_bounded(ptx::smem_u32(&full[warp][st]), (phase >> st) & 1u, p.wait_limit_ns);
+                ptx::mbar_wait_bounded(bar_at + 8 * st, (phase >> st) & 1u, p.wait_limit_ns);
               __syncwarp();
             }
           }
         }
-        const bool skip = dead || ((bad >> stage) & 1u) != 0;
-        if (!skip) {
-          const unsigned char* at = ring + stage * C::kTileBytes;
-          // ---- S^T = K Q^T, per group
-          float s[NT][G][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int u = 0; u < G; ++u)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) s[nt][u][x] = 0.0f;
-          uint32_t ka[2 * G], kb[2 * G];
-          uint32_t par[2][2 * G];  // tokens g, g + 8: (step, low) of K's groups, then V's
-          if (G == 2) {
-            const uint4 a = *reinterpret_cast<const uint4*>(at + g * 64 + t * 16);
-            const uint4 c = *reinterpret_cast<const uint4*>(at + (g + 8) * 64 + t * 16);
-            ka[0] = a.x; ka[1] = a.y; ka[2 * G - 2] = a.z; ka[2 * G - 1] = a.w;
-            kb[0] = c.x; kb[1] = c.y; kb[2 * G - 2] = c.z; kb[2 * G - 1] = c.w;
-            const uint4 pa = *reinterpret_cast<const uint4*>(at + L4::kParams + g * 16);
-            const uint4 pc = *reinterpret_cast<const uint4*>(at + L4::kParams + (g + 8) * 16);
-            par[0][0] = pa.x; par[0][1] = pa.y; par[0][2 * G - 2] = pa.z; par[0][2 * G - 1] = pa.w;
-            par[1][0] = pc.x; par[1][1] = pc.y; par[1][2 * G - 2] = pc.z; par[1][2 * G - 1] = pc.w;
+        if (!dead) {
+          const unsigned char* at = ring + stage * C::kUnitBytes;
+          const int tok0 = (unit0 + i) * kUnit;
+          const uint32_t lost = (bad >> (2 * stage)) & 3u;
+          if (lost == 0 && tok0 + kUnit <= len - p.q_len + 1) {
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) attend(at + k * C::kTileBytes, tok0 + k * int4::kTile, std::false_type{});
           } else {
-            const uint2 a = *reinterpret_cast<const uint2*>(at + g * 32 + t * 8);
-            const uint2 c = *reinterpret_cast<const uint2*>(at + (g + 8) * 32 + t * 8);
-            ka[0] = a.x; ka[1] = a.y;
-            kb[0] = c.x; kb[1] = c.y;
-            const uint2 pa = *reinterpret_cast<const uint2*>(at + L4::kParams + g * 8);
-            const uint2 pc = *reinterpret_cast<const uint2*>(at + L4::kParams + (g + 8) * 8);
-            par[0][0] = pa.x; par[0][1] = pa.y;
-            par[1][0] = pc.x; par[1][1] = pc.y;
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k)
+              if ((lost >> k & 1u) == 0) attend(at + k * C::kTileBytes, tok0 + k * int4::kTile, std::true_type{});
           }
-#pragma unroll
-          for (int w = 0; w < 2 * G; ++w) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t a = half ? ka[w] >> 8 : ka[w], c = half ? kb[w] >> 8 : kb[w];
-              const uint32_t frag[4] = {a & kLo, c & kLo, a & kHi, c & kHi};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                ptx::mma_f16_16816(s[nt][w / 2], frag, qf[nt][2 * w + half][0], qf[nt][2 * w + half][1]);
-            }
-          }
-          float step[2][2][G], low[2][2][G];  // [token g, g + 8][K, V][group]
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-              for (int u = 0; u < G; ++u) {
-                step[r][kv][u] = __uint_as_float(par[r][kv * G + u] << 16);
-                low[r][kv][u] = __uint_as_float(par[r][kv * G + u] & 0xffff0000u);
-              }
-          // scores in units of log2
-          float sc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int r = x / 2, c = x % 2;
-              float dot = s[nt][0][x] * step[r][0][0], bias = low[r][0][0] * qs[nt][0][c];
-              if (G == 2) {
-                dot = fmaf(s[nt][G - 1][x], step[r][0][G - 1], dot);
-                bias = fmaf(low[r][0][G - 1], qs[nt][G - 1][c], bias);
-              }
-              sc[nt][x] = fmaf(dot, h[nt][c], bias);
-            }
-          // A tile in which some row's window ends: tokens past the sequence have no parameters,
-          // rows do not see tokens past their own window.
-          const int tok0 = (tile + i) * int4::kTile;
-          const bool ends = tok0 + int4::kTile > len - p.q_len + 1;
-          if (ends) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if (tok0 + g + 8 * r >= len) {
-#pragma unroll
-                for (int u = 0; u < G; ++u) step[r][1][u] = low[r][1][u] = 0.0f;
-              }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (tok0 + g + 8 * (x / 2) >= lim[nt][x % 2]) sc[nt][x] = -INFINITY;
-          }
-          // ---- weights; the reference moves only when a score passes it by 2^8
-          float pr[NT][4], w[NT][G][4];
-          bool up = false;
-          auto weigh = [&]() {
-            up = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                pr[nt][x] = ptx::ex2(sc[nt][x] - ref[nt][x % 2]);
-                up |= pr[nt][x] > 256.0f;
-#pragma unroll
-                for (int u = 0; u < G; ++u) {
-                  w[nt][u][x] = pr[nt][x] * (step[x / 2][1][u] * F[nt][u][x % 2]);
-                  up |= w[nt][u][x] > 32768.0f;
-                }
-              }
-          };
-          weigh();
-          if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float top = fmaxf(ref[nt][c], fmaxf(sc[nt][c], sc[nt][c + 2]));
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                const float a = ptx::ex2(ref[nt][c] - top);
-                ref[nt][c] = top;
-                l[nt][c] *= a;
-#pragma unroll
-                for (int u = 0; u < G; ++u) {
-                  pm[nt][u][c] *= a;
-                  float big = fmaxf(ptx::ex2(sc[nt][c] - top) * step[0][1][u], ptx::ex2(sc[nt][c + 2] - top) * step[1][1][u]);
-#pragma unroll
-                  for (int d = 4; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-                  const float f = inverse_pow2(fmaxf(big, a / F[nt][u][c]));
-                  const float scale = a / F[nt][u][c] * f;
-                  F[nt][u][c] = f;
-#pragma unroll
-                  for (int m = 0; m < 4; ++m) {
-                    o[4 * u + m][nt][c] *= scale;
-                    o[4 * u + m][nt][c + 2] *= scale;
-                  }
-                }
-              }
-            weigh();
-          }
-          uint32_t pb16[NT][G][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (ends) {  // what a row does not see adds nothing, whatever its value
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (sc[nt][x] == -INFINITY) {
-#pragma unroll
-                  for (int u = 0; u < G; ++u) w[nt][u][x] = 0.0f;
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              l[nt][x % 2] += pr[nt][x];
-#pragma unroll
-              for (int u = 0; u < G; ++u)
-                if (!ends || sc[nt][x] != -INFINITY) pm[nt][u][x % 2] = fmaf(pr[nt][x], low[x / 2][1][u], pm[nt][u][x % 2]);
-            }
-#pragma unroll
-            for (int u = 0; u < G; ++u) {
-              pb16[nt][u][0] = ptx::movmatrix_trans(ptx::pack_f16x2(w[nt][u][0], w[nt][u][1]));
-              pb16[nt][u][1] = ptx::movmatrix_trans(ptx::pack_f16x2(w[nt][u][2], w[nt][u][3]));
-            }
-          }
-          // ---- O^T += V^T P^T: tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of this thread's channels
-          uint32_t v[4][G];
-          const unsigned char* vat = at + L4::kVCodes + (g / (8 / G)) * 512 + t * 32 + (g % (8 / G)) * (4 * G);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (G == 2) {
-              const uint2 a = *reinterpret_cast<const uint2*>(vat + q * 128);
-              v[q][0] = a.x;
-              v[q][G - 1] = a.y;
-            } else {
-              v[q][0] = *reinterpret_cast<const uint32_t*>(vat + q * 128);
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < G; ++u)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const uint32_t sel = m < 2 ? 0x5410u : 0x7632u;
-              uint32_t a = prmt(v[0][u], v[1][u], sel), c = prmt(v[2][u], v[3][u], sel);
-              if (m % 2) {
-                a >>= 8;
-                c >>= 8;
-              }
-              const uint32_t frag[4] = {a & kLo, a & kHi, c & kLo, c & kHi};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) ptx::mma_f16_16816(o[4 * u + m][nt], frag, pb16[nt][u][0], pb16[nt][u][1]);
-            }
         }
         phase ^= 1u << stage;
         stage = stage + 1 == C::kStages ? 0 : stage + 1;
@@ -567,7 +615,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           }
       const bool whole = count == n;
       // only the first piece of a range can be cut and not reach its end; at the end the ring is idle
-      float* rec = rec_of[pos + count < end ? 0 : 1];
+      float* rec = rec_of[count < left ? 0 : 1];
       __syncwarp();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -577,7 +625,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           const float inv = l[nt][c] != 0.0f ? 1.0f / l[nt][c] : 0.0f;  // NaN stays NaN
 #pragma unroll
           for (int u = 0; u < G; ++u) {
-            const float even = 0x1p24f / F[nt][u][c], odd = 0x1p20f / F[nt][u][c];
+            const float even = 0x1p24f / F[nt][c], odd = 0x1p20f / F[nt][c];
             float y[8];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -606,14 +654,15 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
         }
       if (!whole && lane == 0) {
         Piece& pc = pieces[2 * warp + (rec == rec_of[1])];
-        pc.start = pos - tile;
-        pc.tiles = n;
+        pc.start = pos - unit0;
+        pc.units = n;
         pc.b = b;
         pc.seg = seg;
       }
       pos += count;
-      tile = 0;
-      if (pos < end && ++seg == segs) {
+      left -= count;
+      unit0 = 0;
+      if (left > 0 && ++seg == segs) {
         seg = 0;
         len = next_len(p, b);
       }
@@ -638,16 +687,16 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   const int64_t slot_floats = C::kRecFloats;
   int outward[2] = {-1, -1};  // pieces whose segment goes on in another CTA: started before, ends after
   for (int i = 0; i < 2 * kWarps;) {
-    if (pieces[i].tiles == 0) {
+    if (pieces[i].units == 0) {
       ++i;
       continue;
     }
     const Piece pc = pieces[i];
     uint32_t mine = 0;  // records of this segment
     int j = i;
-    for (; j < 2 * kWarps && (pieces[j].tiles == 0 || pieces[j].start == pc.start); ++j)
-      if (pieces[j].tiles != 0) mine |= 1u << j;
-    const bool inside = pc.start >= cta_start && pc.start + pc.tiles <= cta_end;
+    for (; j < 2 * kWarps && (pieces[j].units == 0 || pieces[j].start == pc.start); ++j)
+      if (pieces[j].units != 0) mine |= 1u << j;
+    const bool inside = pc.start >= cta_start && pc.start + pc.units <= cta_end;
     const int slot = pc.start < cta_start ? 0 : 1;
     if (!inside) outward[slot] = i;
     for (int r = warp; r < C::kRows; r += kWarps) {
@@ -689,7 +738,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     if (i >= 0) {
       const Piece pc = pieces[i];
       const int first = static_cast<int>(owner_of(pc.start) / kWarps);
-      const int ctas = static_cast<int>(owner_of(pc.start + pc.tiles - 1) / kWarps) - first + 1;
+      const int ctas = static_cast<int>(owner_of(pc.start + pc.units - 1) / kWarps) - first + 1;
       last = atomicAdd(p.counters + first, 1) == ctas - 1;
     }
     last_of[threadIdx.x] = last;
@@ -700,7 +749,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     __threadfence();
     const Piece pc = pieces[outward[k]];
     const int first = static_cast<int>(owner_of(pc.start) / kWarps);
-    const int last = static_cast<int>(owner_of(pc.start + pc.tiles - 1) / kWarps);
+    const int last = static_cast<int>(owner_of(pc.start + pc.units - 1) / kWarps);
     if (threadIdx.x == 0) p.counters[first] = 0;
     for (int r = warp; r < C::kRows; r += kWarps) {
       bool valid;
