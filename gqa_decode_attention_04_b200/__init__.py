@@ -560,83 +560,118 @@ def decode_step_fp8(q, k_new, v_new, k_pages, v_pages, k_scales, v_scales, block
 
 # ------------------------------------------------------------------ rotating appends, 4-bit cache
 class _on:
-    """Makes dev, and the given stream where there is one, current; .ptr is the stream to launch on.
+    """Makes dev, and the given stream where there is one, current; gives the stream to launch on.
     What a call allocates itself is made inside, so it belongs to the stream that it is used on."""
 
-    __slots__ = ("ptr", "_guards")
+    __slots__ = ("ptr", "guards")
 
     def __init__(self, dev, stream):
-        self._guards = ()
-        if stream is not None:
+        index = dev.index
+        if stream is None and index == _current_device():
+            self.ptr, self.guards = _current_stream(index), None
+        elif stream is None:
+            self.ptr, self.guards = _current_stream(index), (torch.cuda.device(dev),)
+        else:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=dev)
-            self.ptr = stream.cuda_stream
-            self._guards = (torch.cuda.device(dev), torch.cuda.stream(stream))
-        else:
-            self.ptr = torch.cuda.current_stream(dev).cuda_stream
-            if dev.index != torch.cuda.current_device():
-                self._guards = (torch.cuda.device(dev),)
+            self.ptr, self.guards = stream.cuda_stream, (torch.cuda.device(dev), torch.cuda.stream(stream))
 
     def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
+        if self.guards is not None:
+            for g in self.guards:
+                g.__enter__()
         return self.ptr
 
     def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
+        if self.guards is not None:
+            for g in reversed(self.guards):
+                g.__exit__(*exc)
         return False
 
 
-def _need_rows(t, name, shape, dev):
-    """bf16 rows [T, heads, head_dim], contiguous but for the stride between tokens."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must be [num_tokens, heads, head_dim]" + (f" = {list(shape)}" if shape else ""))
-    T, h, d = t.shape
-    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+def _current_device() -> int:
+    return torch.cuda.current_device()
+
+
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same, 2 us sooner: as torch's own launchers ask
+    _current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _is(t, dtype, dev) -> bool:
+    """_need's conditions, without its messages: the calls below ask this first."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev.index
+            and t.is_contiguous())
+
+
+def _all(dev, *wanted) -> None:
+    """(tensor, name, dtype) triples that _need is to hold for."""
+    for t, name, dtype in wanted:
+        if not _is(t, dtype, dev):
+            _need(t, name, dtype, dev)
+
+
+def _need_rows(t, name, heads, dim, tokens, dev):
+    """bf16 rows [tokens, heads, dim], contiguous but for the stride between tokens, which is returned
+    (in elements).  heads, tokens None: any."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda and t.get_device() == dev.index):
+        _need(t.contiguous() if isinstance(t, torch.Tensor) else t, name, torch.bfloat16, dev)
+    shape = t.shape
+    if (len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads)
+            or (tokens is not None and shape[0] != tokens)):
+        raise ValueError(f"{name} must be [num_tokens, heads, head_dim] = [{tokens or 'T'}, {heads or 'H'}, {dim}], "
+                         f"got {list(shape)}")
+    if t.is_contiguous() or 0 in shape:
+        return shape[1] * dim
+    stride = t.stride()
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if T > 1 else h * d
+    return stride[0] if shape[0] > 1 else shape[1] * dim
 
 
 def _rope(fn, q, k_new, v_new, cos_sin, pools, scales, block_table, positions, seq_ids, interleaved, q_out, stream,
           pool_shape):
     dev = pools[0].device
     P, Hk, ps, D = pool_shape
-    q_stride = _need_rows(q, "q", None, dev)
-    T, H, Dq = q.shape
-    if Dq != D:
-        raise ValueError("q's head_dim differs from the pools'")
-    k_stride = _need_rows(k_new, "k_new", (T, Hk, D), dev)
-    v_stride = _need_rows(v_new, "v_new", (T, Hk, D), dev)
-    _need(cos_sin, "cos_sin", torch.float32, dev)
+    q_stride = _need_rows(q, "q", None, D, None, dev)
+    T, H, _ = q.shape
+    k_stride = _need_rows(k_new, "k_new", Hk, D, T, dev)
+    v_stride = _need_rows(v_new, "v_new", Hk, D, T, dev)
+    _all(dev, (cos_sin, "cos_sin", torch.float32), (block_table, "block_table", torch.int32),
+         (positions, "positions", torch.int32))
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_positions, rotary_dim]")
-    _need(block_table, "block_table", torch.int32, dev)
-    _need(positions, "positions", torch.int32, dev)
-    if block_table.dim() != 2 or tuple(positions.shape) != (T,):
+    if block_table.dim() != 2 or positions.dim() != 1 or positions.shape[0] != T:
         raise ValueError("block_table must be [num_seqs, max_blocks], positions [num_tokens]")
+    seqs, blocks = block_table.shape
+    ids = None
     if seq_ids is not None:
-        _need(seq_ids, "seq_ids", torch.int32, dev)
-        if tuple(seq_ids.shape) != (T,):
+        _all(dev, (seq_ids, "seq_ids", torch.int32))
+        if seq_ids.dim() != 1 or seq_ids.shape[0] != T:
             raise ValueError("seq_ids must be [num_tokens]")
-    elif block_table.shape[0] != T:
+        ids = seq_ids.data_ptr()
+    elif seqs != T:
         raise ValueError("without seq_ids, token t is sequence t: block_table must have num_tokens rows")
+    max_positions, rotary = cos_sin.shape
     with _on(dev, stream) as ptr:
-        q_out = _multi_out(q_out, (T, H, D), dev)
+        q_out = _out(q_out, (T, H, D), dev)
         _check(fn(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), cos_sin.data_ptr(), q_out.data_ptr(),
-                  *(t.data_ptr() for t in (*pools, *scales)), block_table.data_ptr(), positions.data_ptr(),
-                  None if seq_ids is None else seq_ids.data_ptr(), T, block_table.shape[0], H, Hk, D, cos_sin.shape[1],
-                  1 if interleaved else 0, cos_sin.shape[0], q_stride, k_stride, v_stride, ps, block_table.shape[1], P,
+                  *(t.data_ptr() for t in (*pools, *scales)), block_table.data_ptr(), positions.data_ptr(), ids, T, seqs,
+                  H, Hk, D, rotary, 1 if interleaved else 0, max_positions, q_stride, k_stride, v_stride, ps, blocks, P,
                   ptr))
     return q_out
+
+
+def _out(out, shape, dev):
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _all(dev, (out, "out", torch.bfloat16))
+    if out.shape != shape:
+        raise ValueError(f"out must be {list(shape)}")
+    return out
 
 
 def rope_kv_append(q, k_new, v_new, cos_sin, k_pages, v_pages, block_table, positions,
@@ -651,9 +686,8 @@ def rope_kv_append(q, k_new, v_new, cos_sin, k_pages, v_pages, block_table, posi
     (q_out, which may be q itself when q is contiguous).  Rows with seq_ids[t] < 0 are padding.
     """
     dev = k_pages.device
-    _need(k_pages, "k_pages", torch.bfloat16, dev)
-    _need(v_pages, "v_pages", torch.bfloat16, dev)
-    if k_pages.dim() != 4 or tuple(v_pages.shape) != tuple(k_pages.shape):
+    _all(dev, (k_pages, "k_pages", torch.bfloat16), (v_pages, "v_pages", torch.bfloat16))
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("page pools must both be [num_pages, num_kv_heads, page_size, head_dim]")
     return _rope(load_library().gqa_rope_kv_append, q, k_new, v_new, cos_sin, (k_pages, v_pages), (), block_table,
                  positions, seq_ids, interleaved, q_out, stream, k_pages.shape)
@@ -670,7 +704,7 @@ def rope_kv_append_fp8(q, k_new, v_new, cos_sin, k_pages, v_pages, k_scales, v_s
 
 
 def _pool_int4(kv_pages, dev):
-    _need(kv_pages, "kv_pages", torch.uint8, dev)
+    _all(dev, (kv_pages, "kv_pages", torch.uint8))
     if kv_pages.dim() != 4 or kv_pages.shape[3] % 18 != 0:
         raise ValueError("kv_pages must be [num_pages, num_kv_heads, page_size / 16, 18 * head_dim] uint8")
     P, Hk, tiles, b = kv_pages.shape
@@ -690,17 +724,16 @@ def quantize_pages_int4(k_pages, v_pages, kv_pages: Optional[torch.Tensor] = Non
     """A pair of bf16 pools as one 4-bit pool [num_pages, num_kv_heads, page_size / 16, 18 * head_dim]
     (uint8; include/gqa_int4.h gives the format)."""
     dev = k_pages.device
-    _need(k_pages, "k_pages", torch.bfloat16, dev)
-    _need(v_pages, "v_pages", torch.bfloat16, dev)
-    if k_pages.dim() != 4 or tuple(v_pages.shape) != tuple(k_pages.shape):
+    _all(dev, (k_pages, "k_pages", torch.bfloat16), (v_pages, "v_pages", torch.bfloat16))
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("page pools must both be [num_pages, num_kv_heads, page_size, head_dim]")
     P, Hk, ps, D = k_pages.shape
     with _on(dev, stream) as ptr:
         if kv_pages is None:
             kv_pages = torch.empty((P, Hk, ps // 16, 18 * D), dtype=torch.uint8, device=dev)
         else:
-            _need(kv_pages, "kv_pages", torch.uint8, dev)
-            if tuple(kv_pages.shape) != (P, Hk, ps // 16, 18 * D):
+            _all(dev, (kv_pages, "kv_pages", torch.uint8))
+            if kv_pages.shape != (P, Hk, ps // 16, 18 * D):
                 raise ValueError(f"kv_pages must be {[P, Hk, ps // 16, 18 * D]}")
         _check(load_library().gqa_kv_quantize_int4(k_pages.data_ptr(), v_pages.data_ptr(), kv_pages.data_ptr(), P, Hk,
                                                    ps, D, ptr))
@@ -713,7 +746,7 @@ def dequantize_pages_int4(kv_pages, k_pages: Optional[torch.Tensor] = None, v_pa
     dev = kv_pages.device
     P, Hk, ps, D = shape = _pool_int4(kv_pages, dev)
     with _on(dev, stream) as ptr:
-        k_pages, v_pages = _multi_out(k_pages, shape, dev), _multi_out(v_pages, shape, dev)
+        k_pages, v_pages = _out(k_pages, shape, dev), _out(v_pages, shape, dev)
         _check(load_library().gqa_kv_dequantize_int4(kv_pages.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), P,
                                                      Hk, ps, D, ptr))
     return k_pages, v_pages
@@ -723,11 +756,10 @@ def kv_append_int4(k_new, v_new, kv_pages, block_table, positions, stream=None) 
     """Write k_new/v_new [B, Hk, D] (bf16) into the 4-bit pool at positions[b]."""
     dev = kv_pages.device
     P, Hk, ps, D = _pool_int4(kv_pages, dev)
-    for t, n, dt in ((k_new, "k_new", torch.bfloat16), (v_new, "v_new", torch.bfloat16),
-                     (block_table, "block_table", torch.int32), (positions, "positions", torch.int32)):
-        _need(t, n, dt, dev)
+    _all(dev, (k_new, "k_new", torch.bfloat16), (v_new, "v_new", torch.bfloat16),
+         (block_table, "block_table", torch.int32), (positions, "positions", torch.int32))
     B = k_new.shape[0]
-    if tuple(k_new.shape) != (B, Hk, D) or tuple(v_new.shape) != (B, Hk, D):
+    if k_new.shape != (B, Hk, D) or v_new.shape != (B, Hk, D):
         raise ValueError("k_new / v_new must be [num_seqs, num_kv_heads, head_dim]")
     if block_table.dim() != 2 or block_table.shape[0] != B or tuple(positions.shape) != (B,):
         raise ValueError("block_table must be [num_seqs, max_blocks], positions [num_seqs]")
@@ -752,26 +784,25 @@ def _workspace(workspace, dev):
     if workspace is None:  # one of this call's own, on its stream: safe whatever runs beside it
         workspace = torch.empty(load_library().gqa_int4_workspace_bytes(), dtype=torch.uint8, device=dev)
         workspace[:_WORKSPACE_HEAD].zero_()
-    _need(workspace, "workspace", torch.uint8, dev)
+    else:
+        _all(dev, (workspace, "workspace", torch.uint8))
     return workspace
 
 
 def _attend_int4(q, kv_pages, block_table, seq_lens, out, scale, workspace, stream, multi):
     dev = q.device
-    _need(q, "q", torch.bfloat16, dev)
+    _all(dev, (q, "q", torch.bfloat16), (block_table, "block_table", torch.int32), (seq_lens, "seq_lens", torch.int32))
     P, Hk, ps, D = _pool_int4(kv_pages, dev)
-    _need(block_table, "block_table", torch.int32, dev)
-    _need(seq_lens, "seq_lens", torch.int32, dev)
     if q.dim() != (4 if multi else 3) or q.shape[-1] != D:
         raise ValueError("q must be [num_seqs, %snum_heads, head_dim] with the pool's head_dim" % ("q_len, " if multi else ""))
     B, H = q.shape[0], q.shape[-2]
-    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(seq_lens.shape) != (B,):
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("block_table must be [num_seqs, max_blocks], seq_lens [num_seqs]")
     if scale is None:
         scale = 1.0 / (D ** 0.5)
     lib = load_library()
     with _on(dev, stream) as ptr:
-        out = _multi_out(out, q.shape, dev)
+        out = _out(out, q.shape, dev)
         ws = _workspace(workspace, dev)
         fn = lib.gqa_paged_multi_query_attn_int4 if multi else lib.gqa_paged_decode_attn_int4
         _check(fn(q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), B,
@@ -805,21 +836,20 @@ def decode_step_int4(q, k_new, v_new, kv_pages, block_table, positions, seq_lens
     the rotated q.
     """
     dev = q.device
+    _all(dev, (q, "q", torch.bfloat16), (k_new, "k_new", torch.bfloat16), (v_new, "v_new", torch.bfloat16),
+         (block_table, "block_table", torch.int32), (positions, "positions", torch.int32),
+         (seq_lens, "seq_lens", torch.int32))
     P, Hk, ps, D = _pool_int4(kv_pages, dev)
-    for t, n, dt in ((q, "q", torch.bfloat16), (k_new, "k_new", torch.bfloat16), (v_new, "v_new", torch.bfloat16),
-                     (block_table, "block_table", torch.int32), (positions, "positions", torch.int32),
-                     (seq_lens, "seq_lens", torch.int32)):
-        _need(t, n, dt, dev)
     if q.dim() != 3 or q.shape[2] != D:
         raise ValueError("q must be [num_seqs, num_heads, head_dim] with the pool's head_dim")
     B, H = q.shape[0], q.shape[1]
-    if tuple(k_new.shape) != (B, Hk, D) or tuple(v_new.shape) != (B, Hk, D):
+    if k_new.shape != (B, Hk, D) or v_new.shape != (B, Hk, D):
         raise ValueError("k_new / v_new must be [num_seqs, num_kv_heads, head_dim]")
-    if (block_table.dim() != 2 or block_table.shape[0] != B or tuple(seq_lens.shape) != (B,)
-            or tuple(positions.shape) != (B,)):
+    if (block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,)
+            or positions.shape != (B,)):
         raise ValueError("block_table must be [num_seqs, max_blocks]; seq_lens, positions [num_seqs]")
     if cos_sin is not None:
-        _need(cos_sin, "cos_sin", torch.float32, dev)
+        _all(dev, (cos_sin, "cos_sin", torch.float32))
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_positions, rotary_dim]")
     elif q_rot is not None:
@@ -827,9 +857,9 @@ def decode_step_int4(q, k_new, v_new, kv_pages, block_table, positions, seq_lens
     if scale is None:
         scale = 1.0 / (D ** 0.5)
     with _on(dev, stream) as ptr:
-        out = _multi_out(out, (B, H, D), dev)
+        out = _out(out, (B, H, D), dev)
         if cos_sin is not None:
-            q_rot = _multi_out(q_rot, (B, H, D), dev)
+            q_rot = _out(q_rot, (B, H, D), dev)
         ws = _workspace(workspace, dev)
         _check(load_library().gqa_decode_step_int4(
             q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), None if cos_sin is None else cos_sin.data_ptr(),

@@ -36,6 +36,7 @@
 // Safety: every wait is bounded; a warp whose wait runs out sets the error word, treats the rest
 // of its range as masked, drains its own copies (bounded) and still takes part in the merges, so
 // no counter is left behind.  Page ids and lengths are range-checked before use.
+#include <atomic>
 #include <type_traits>
 
 #include "int4_codec.cuh"
@@ -47,6 +48,7 @@ namespace gqa {
 namespace {
 
 constexpr int kWarps = 8;
+static_assert((2 * kWarps & (2 * kWarps - 1)) == 0 && 2 * kWarps <= 32, "a lane per piece of the CTA");
 constexpr float kNone = -3.0e38f;   // reference of a row that has seen no token
 
 template <int D, int NT>
@@ -55,13 +57,12 @@ struct Cfg {
   static constexpr int kGroups = D / 64;
   static constexpr int kTileBytes = 18 * D;
   static constexpr int kUnitBytes = 2 * kTileBytes;
-  static constexpr int kStages = NT == 1 ? 2 : 4;
+  static constexpr int kStages = NT == 1 ? 3 : 5;
   static constexpr int kCtas = NT == 1 ? 2 : 1;     // per SM
   static constexpr int kRecFloats = kRows * (D + 2);  // a piece: [rows][D], then (reference, sum)
   static constexpr int kRingBytes = kStages * kUnitBytes;
   static_assert(kRingBytes >= kRecFloats * 4, "the last piece of a warp is left in its ring");
-  static constexpr int kRecBytes = (kRecFloats * 4 + 127) / 128 * 128;
-  static constexpr int kSmem = kWarps * (kRingBytes + kRecBytes);
+  static constexpr int kSmem = kWarps * kRingBytes;
 };
 
 // A piece that a warp's range cut off.
@@ -73,7 +74,14 @@ struct Piece {
 
 constexpr int kUnit = 2 * int4::kTile;  // tokens per step of a warp
 
+// What a segment costs a warp beside its units, in units: fetching q, ending and leaving a piece.
+// The list is cut by it, since some warps get dozens of short sequences: 256 sequences of 1 to 32768
+// tokens took 266 us with 0, 208 with 1, 182 with 2, 183 with 4; a batch of 32 of 512 to 4096 tokens
+// 37.9, 36.6, 36.0, 36.1, and with four query tokens 61, 51.9, 50.6, 48.7.
+constexpr int kSegCost = 3;
+
 __device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int cost_of(int len) { return len > 0 ? units_of(len) + kSegCost : 0; }
 
 // The length of sequence b, 0 if it is out of range.
 __device__ __forceinline__ int checked_len(const Int4DecodeParams& p, int b) {
@@ -89,6 +97,22 @@ __device__ __forceinline__ int next_len(const Int4DecodeParams& p, int& b) {
   }
   return max(len, 1);
 }
+
+// a / b, both not negative; in 32 bits where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// How the list of `total` units is cut: the first `rem` workers take per + 1 units, the others per.
+struct Split {
+  int64_t total, workers, per, rem;
+  __device__ __forceinline__ int64_t start(int64_t w) const { return w >= workers ? total : w * per + min(w, rem); }
+  __device__ __forceinline__ int64_t owner(int64_t unit) const {
+    const int64_t cut = rem * (per + 1);
+    return unit < cut ? quotient(unit, per + 1) : rem + quotient(unit - cut, per);
+  }
+};
 
 // The query token of row r of a kv head.
 __device__ __forceinline__ int token_of(const Int4DecodeParams& p, int r) { return p.q_len == 1 ? 0 : r / p.group; }
@@ -124,14 +148,18 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   __shared__ int64_t scan[kWarps];
   __shared__ __align__(8) uint64_t full[kWarps][C::kStages];
   __shared__ Piece pieces[2 * kWarps];
-  __shared__ int last_of[2];
+  __shared__ int2 last_of[2];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   unsigned char* ring = smem + warp * C::kRingBytes;
-  float* rec_of[2];
-  rec_of[0] = reinterpret_cast<float*>(smem + kWarps * C::kRingBytes + warp * C::kRecBytes);
-  rec_of[1] = reinterpret_cast<float*>(ring);
+  // A warp's pieces: one cut at the front goes to its workspace slot, one cut at the end stays in
+  // its ring, which is idle by then.
+  const int64_t cta_slots = 2 * static_cast<int64_t>(gridDim.x) * C::kRecFloats;
+  auto record = [&](int i) {
+    return (i & 1) ? reinterpret_cast<float*>(smem + (i / 2) * C::kRingBytes)
+                   : p.slots + cta_slots + (static_cast<int64_t>(blockIdx.x) * kWarps + i / 2) * C::kRecFloats;
+  };
 
   if (lane == 0) {
 #pragma unroll
@@ -147,7 +175,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   {
     int64_t mine = 0;
     const int b0 = threadIdx.x * chunk, b1 = min(p.num_seqs, b0 + chunk);
-    for (int b = b0; b < b1; ++b) mine += units_of(checked_len(p, b));
+    for (int b = b0; b < b1; ++b) mine += cost_of(checked_len(p, b));
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -161,104 +189,110 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     excl[threadIdx.x] = before + incl - mine;
     __syncthreads();
   }
-  int64_t total = 0;
-  for (int w = 0; w < kWarps; ++w) total += scan[w];
-  total *= segs;
-  // as many warps as there are tiles, if that is fewer
-  const int64_t workers = min(static_cast<int64_t>(gridDim.x) * kWarps, total);
-  auto start_of = [&](int64_t w) { return w >= workers ? total : total * w / workers; };
-  auto owner_of = [&](int64_t tile) { return ((tile + 1) * workers - 1) / total; };
+  Split split;
+  {
+    int64_t total = 0;
+    for (int w = 0; w < kWarps; ++w) total += scan[w];
+    split.total = total * segs;
+    // as many warps as there are units, if that is fewer
+    split.workers = min(static_cast<int64_t>(gridDim.x) * kWarps, split.total);
+    split.per = split.total == 0 ? 0 : quotient(split.total, split.workers);
+    split.rem = split.total - split.per * split.workers;
+  }
   const int64_t me = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  int64_t pos = start_of(me);
-  const int64_t end = start_of(me + 1);
+  int64_t pos = split.start(me);
+  const int64_t end = split.start(me + 1);
 
   ptx::pdl_wait_prerequisites();  // q and the pool may be written by the preceding append
 
-  // Rows of sequences without a token (a length out of range counts as none and is reported).
-  for (int64_t b = me; b < p.num_seqs; b += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int raw = __ldg(p.seq_lens + b);
-    if (checked_len(p, static_cast<int>(b)) != 0) continue;
-    if (raw != 0 && lane == 0) atomicOr(p.err, kErrBounds);
-    uint4* o = reinterpret_cast<uint4*>(p.out + b * p.q_len * p.num_heads * D);
-    for (int i = lane; i < p.q_len * p.num_heads * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
-  }
-
   if (pos < end) {
     // ---- find the first tile: the chunk, then the sequence in it
-    const int64_t unit = pos / segs;  // in tiles per row tile
+    const int64_t unit = quotient(pos, segs);  // in units of a sequence's one segment
     int ci = 0;
     for (int i = 0; i < kWarps; ++i) {
       const unsigned m = __ballot_sync(0xffffffffu, excl[32 * i + lane] <= unit);
       ci += __popc(m);
     }
-    int b = (ci - 1) * chunk;
+    int b = (ci - 1) * chunk, len = 0;
     int64_t base = excl[ci - 1];
-    int len = 0;
-    for (;; b += 32) {
-      const int mine = b + lane < p.num_seqs ? checked_len(p, b + lane) : 0;
-      int64_t incl = units_of(mine);
+    if (chunk == 1) {
+      len = checked_len(p, b);
+    } else {
+      for (;; b += 32) {
+        const int mine = b + lane < p.num_seqs ? checked_len(p, b + lane) : 0;
+        int64_t incl = cost_of(mine);
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += o;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + incl > unit);
+        if (past != 0) {
+          const int at = __ffs(past) - 1;
+          b += at;
+          len = __shfl_sync(0xffffffffu, mine, at);
+          base += __shfl_sync(0xffffffffu, incl, at) - cost_of(len);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+        if (b + 32 >= p.num_seqs) break;  // only if the lengths changed under the call
       }
-      const unsigned past = __ballot_sync(0xffffffffu, base + incl > unit);
-      if (past != 0) {
-        const int at = __ffs(past) - 1;
-        b += at;
-        len = __shfl_sync(0xffffffffu, mine, at);
-        base += __shfl_sync(0xffffffffu, incl, at) - units_of(len);
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, incl, 31);
-      if (b + 32 >= p.num_seqs) break;  // only if the lengths changed under the call
     }
-    if (len == 0) pos = end;
-    int seg = static_cast<int>((pos - base * segs) / max(1, units_of(len)));
-    int unit0 = static_cast<int>(pos - base * segs - static_cast<int64_t>(seg) * units_of(len));
-    int left = static_cast<int>(min(end - pos, int64_t{INT32_MAX}));  // units to do
+    // The position lies in segment seg's own cost (then its first unit is the next) or is a unit of it.
+    int seg = static_cast<int>(quotient(pos - base * segs, max(1, cost_of(len))));
+    const int into = static_cast<int>(pos - base * segs - static_cast<int64_t>(seg) * cost_of(len));
+    int unit0 = max(0, into - kSegCost);
+    int64_t first = pos - into + kSegCost;  // the position of the segment's first unit
+    // positions from unit0 to the end of the range
+    int left = len == 0 ? 0 : static_cast<int>(min(end - first - unit0, int64_t{INT32_MAX}));
 
-    // ---- the copies' cursor runs kStages units ahead of the arithmetic's.  Lanes 0 and 1 bring
-    // one tile each of a unit.
-    int pb = b, phead = seg / p.n_rt, prt = seg - phead * p.n_rt, punit = unit0, plen = len, pleft = left;
-    int win = -1, win_b = -1;  // first block and sequence of the block-table window (one entry per lane)
-    int entry = 0, pstage = 0;
-    uint32_t bad = 0, phase = 0;  // two bits per stage: no data behind the tile; bit per stage: parity to wait for
-    const uint32_t ring_at = ptx::smem_u32(ring), bar_at = ptx::smem_u32(&full[warp][0]);
+    // ---- the copies' cursor runs kStages units ahead of the arithmetic's.  Lane i holds the address
+    // of tile win + i of the cursor's segment (0: none) and issues that tile's copy itself.
+    int pb = b, phead = seg / p.n_rt, prt = seg - phead * p.n_rt, plen = len, pleft = left;
+    int punits = units_of(len) - unit0;  // units of the segment not issued yet
+    int win = 2 * unit0, in_win = 16;    // the window's first tile; its next unit (16: past it)
+    int pstage = 0, ahead = -1;          // ahead: this lane's page of the next window
+    uint32_t bad = 0;                    // two bits per stage: no data behind the tile
+    uint64_t addr = 0;
+    const uint32_t ring_at = ptx::smem_u32(ring) + (lane & 1) * C::kTileBytes, bar_at = ptx::smem_u32(&full[warp][0]);
+    auto page_of = [&](int tile) {
+      const int block = p.tpp_magic != 0 ? fast_div(tile, p.tpp_magic, p.tpp_shift) : tile;
+      return tile * int4::kTile < plen ? __ldg(p.block_table + static_cast<int64_t>(pb) * p.max_blocks + block) : -1;
+    };
     auto produce = [&]() {
       if (pleft <= 0) return;
-      const int ptile = 2 * punit + (lane & 1);
-      const int block = p.tpp_magic != 0 ? fast_div(ptile, p.tpp_magic, p.tpp_shift) : ptile;
-      const int block0 = p.tpp_magic != 0 ? fast_div(2 * punit, p.tpp_magic, p.tpp_shift) : 2 * punit;
-      // (31: the unit's second tile may be in the next block)
-      if (pb != win_b || static_cast<unsigned>(block0 - win) >= 31u) {
-        win = block0;
-        win_b = pb;
-        entry = win + lane < p.max_blocks ? __ldg(p.block_table + static_cast<int64_t>(pb) * p.max_blocks + win + lane) : -1;
+      if (in_win == 16) {  // the next 32 tiles
+        const int tile = win + lane;
+        const int block = p.tpp_magic != 0 ? fast_div(tile, p.tpp_magic, p.tpp_shift) : tile;
+        const int page = ahead;
+        const bool wanted = tile * int4::kTile < plen;
+        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
+        const uint32_t at = (static_cast<uint32_t>(page) * p.num_kv_heads + phead) * p.tiles_per_page +
+                            (tile - block * p.tiles_per_page);
+        addr = ok && wanted ? reinterpret_cast<uint64_t>(p.pool) + static_cast<uint64_t>(at) * C::kTileBytes : 0;
+        // (only tiles of this warp's range are its to report)
+        if (wanted && !ok && lane < 2 * min(pleft, 16)) atomicOr(p.err, kErrBounds);
+        in_win = 0;
+        win += 32;
+        ahead = page_of(win + lane);
       }
-      const int page = __shfl_sync(0xffffffffu, entry, block - win);
-      const bool wanted = ptile * int4::kTile < plen;  // (the last unit may be one tile)
-      const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-      const unsigned lost = __ballot_sync(0xffffffffu, !ok || !wanted) & 3u;
-      bad = (bad & ~(3u << (2 * pstage))) | (lost << (2 * pstage));
-      if (lane < 2) {
+      const uint32_t here = __ballot_sync(0xffffffffu, addr != 0) >> (2 * in_win);
+      bad = (bad & ~(3u << (2 * pstage))) | ((~here & 3u) << (2 * pstage));
+      if ((lane >> 1) == in_win) {
         const uint32_t bar = bar_at + 8 * pstage;
-        if (ok && wanted) {
-          const uint32_t at = (static_cast<uint32_t>(page) * p.num_kv_heads + phead) * p.tiles_per_page +
-                              (ptile - block * p.tiles_per_page);
+        if (addr != 0) {
           ptx::mbar_arrive_expect_tx(bar, C::kTileBytes);
           if (!p.arm_without_copy)
-            ptx::bulk_load(ring_at + pstage * C::kUnitBytes + lane * C::kTileBytes,
-                           p.pool + static_cast<uint64_t>(at) * C::kTileBytes, C::kTileBytes, bar);
+            ptx::bulk_load(ring_at + pstage * C::kUnitBytes, reinterpret_cast<const void*>(addr), C::kTileBytes, bar);
         } else {
-          if (wanted) atomicOr(p.err, kErrBounds);
           ptx::mbar_arrive(bar);
         }
       }
       pstage = pstage + 1 == C::kStages ? 0 : pstage + 1;
+      ++in_win;
       --pleft;
-      if (++punit == units_of(plen)) {
-        punit = 0;
+      if (--punits == 0) {  // the next segment
+        pleft -= kSegCost;
         if (++prt == p.n_rt) {
           prt = 0;
           if (++phead == p.num_kv_heads) {
@@ -266,12 +300,22 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
             if (pleft > 0) plen = next_len(p, pb);
           }
         }
+        punits = units_of(plen);
+        win = 0;
+        in_win = 16;
+        if (pleft > 0) ahead = page_of(lane);
       }
     };
+    ahead = page_of(win + lane);
     __syncwarp();
     for (int s = 0; s < C::kStages; ++s) produce();
 
+    // this lane's places in a tile
+    const uint32_t at_k = g * (D / 2) + t * (D / 8), at_par = L4::kParams + g * (8 * G);
+    const uint32_t at_v = L4::kVCodes + (g / (8 / G)) * 512 + t * 32 + (g % (8 / G)) * (4 * G);
+    const uint32_t ring0 = ptx::smem_u32(ring);
     int stage = 0;
+    uint32_t parity = 0;
     bool dead = false;
     while (left > 0) {
       // ---- a piece: units [unit0, unit0 + count) of segment (b, seg)
@@ -359,7 +403,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
       }
 
       // One tile whose first token is tok0.  ENDS: some row's window ends in it.
-      auto attend = [&](const unsigned char* at, int tok0, auto ends_tag) {
+      auto attend = [&](uint32_t at, int tok0, auto ends_tag) {
         constexpr bool ENDS = decltype(ends_tag)::value;
         // ---- S^T = K Q^T per group, and the minima's part of it
         float s[NT][G][4], bias[NT][4];
@@ -374,21 +418,17 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
         uint32_t ka[2 * G], kb[2 * G];
         uint32_t par[2][2 * G];  // tokens g, g + 8: (step, low) of K's groups, then V's
         if (G == 2) {
-          const uint4 a = *reinterpret_cast<const uint4*>(at + g * 64 + t * 16);
-          const uint4 c = *reinterpret_cast<const uint4*>(at + (g + 8) * 64 + t * 16);
+          const uint4 a = ptx::lds128(at + at_k), c = ptx::lds128(at + at_k + 8 * 64);
           ka[0] = a.x; ka[1] = a.y; ka[2 * G - 2] = a.z; ka[2 * G - 1] = a.w;
           kb[0] = c.x; kb[1] = c.y; kb[2 * G - 2] = c.z; kb[2 * G - 1] = c.w;
-          const uint4 pa = *reinterpret_cast<const uint4*>(at + L4::kParams + g * 16);
-          const uint4 pc = *reinterpret_cast<const uint4*>(at + L4::kParams + (g + 8) * 16);
+          const uint4 pa = ptx::lds128(at + at_par), pc = ptx::lds128(at + at_par + 8 * 16);
           par[0][0] = pa.x; par[0][1] = pa.y; par[0][2 * G - 2] = pa.z; par[0][2 * G - 1] = pa.w;
           par[1][0] = pc.x; par[1][1] = pc.y; par[1][2 * G - 2] = pc.z; par[1][2 * G - 1] = pc.w;
         } else {
-          const uint2 a = *reinterpret_cast<const uint2*>(at + g * 32 + t * 8);
-          const uint2 c = *reinterpret_cast<const uint2*>(at + (g + 8) * 32 + t * 8);
+          const uint2 a = ptx::lds64(at + at_k), c = ptx::lds64(at + at_k + 8 * 32);
           ka[0] = a.x; ka[1] = a.y;
           kb[0] = c.x; kb[1] = c.y;
-          const uint2 pa = *reinterpret_cast<const uint2*>(at + L4::kParams + g * 8);
-          const uint2 pc = *reinterpret_cast<const uint2*>(at + L4::kParams + (g + 8) * 8);
+          const uint2 pa = ptx::lds64(at + at_par), pc = ptx::lds64(at + at_par + 8 * 8);
           par[0][0] = pa.x; par[0][1] = pa.y;
           par[1][0] = pc.x; par[1][1] = pc.y;
         }
@@ -440,7 +480,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
               seen[nt][x] = tok0 + g + 8 * (x / 2) < lim;
             }
           }
-        // ---- weights; the reference moves only when a score passes it by 2^8
+        // ---- weights; the reference moves only when a score passes it by 12 (in units of log2)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint64_t hh = ptx::f2_pack(h[nt][0], h[nt][1]);
@@ -483,7 +523,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
               big = ptx::max3(big, w[nt][u][2], w[nt][u][3]);
             }
           }
-          up = top > 256.0f || big > 32768.0f;
+          up = top > 4096.0f || big > 32768.0f;
         };
         weigh();
         if (__any_sync(0xffffffffu, up)) {
@@ -508,10 +548,10 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
               }
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-              // the largest weight so far in [2^6, 2^8): 2^8 below the bound, as far as scores may pass
-              // the reference, and 2^20 above fp16's subnormals
+              // the largest weight so far in [2^2, 2^3): 2^12 below the bound, as far as scores may pass
+              // the reference, and 2^16 above fp16's subnormals
               const float before = a / F[nt][c];
-              const float f = inverse_pow2(fmaxf(big * 0x1p-6f, before));
+              const float f = inverse_pow2(fmaxf(big * 0x1p-2f, before));
               const float scale = before * f;
               F[nt][c] = f;
 #pragma unroll
@@ -542,15 +582,14 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
         }
         // ---- O^T += V^T P^T: tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of this thread's channels
         uint32_t v[4][G];
-        const unsigned char* vat = at + L4::kVCodes + (g / (8 / G)) * 512 + t * 32 + (g % (8 / G)) * (4 * G);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (G == 2) {
-            const uint2 a = *reinterpret_cast<const uint2*>(vat + q * 128);
+            const uint2 a = ptx::lds64(at + at_v + q * 128);
             v[q][0] = a.x;
             v[q][G - 1] = a.y;
           } else {
-            v[q][0] = *reinterpret_cast<const uint32_t*>(vat + q * 128);
+            v[q][0] = ptx::lds32(at + at_v + q * 128);
           }
         }
 #pragma unroll
@@ -569,37 +608,38 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           }
       };
 
-      for (int i = 0; i < count; ++i) {
-        if (!dead) {
-          const bool ok = ptx::mbar_wait_bounded(bar_at + 8 * stage, (phase >> stage) & 1u, p.wait_limit_ns);
-          if (!__all_sync(0xffffffffu, ok)) {
-            dead = true;
-            if (lane == 0) atomicOr(p.err, kErrTimeout);
-            if (!p.arm_without_copy) {  // nothing may still be landing when the ring is written or given up
-              const int in_flight = left - pleft - i;
-              for (int k = 0, st = stage; k < in_flight; ++k, st = st + 1 == C::kStages ? 0 : st + 1)
-                ptx::mbar_wait_bounded(bar_at + 8 * st, (phase >> st) & 1u, p.wait_limit_ns);
-              __syncwarp();
+      // units whose tokens every row sees
+      const int open = max(0, len - p.q_len + 1) / kUnit - unit0;
+      for (int i = 0; i < count && !dead; ++i) {
+        const bool landed = ptx::mbar_wait_bounded(bar_at + 8 * stage, parity, p.wait_limit_ns);
+        if (!__all_sync(0xffffffffu, landed)) {
+          dead = true;
+          if (lane == 0) atomicOr(p.err, kErrTimeout);
+          if (!p.arm_without_copy) {  // nothing may still be landing when the ring is written or given up
+            int in_flight = pstage - stage;
+            if (in_flight <= 0) in_flight += C::kStages;
+            for (; in_flight > 0; --in_flight) {
+              ptx::mbar_wait_bounded(bar_at + 8 * stage, parity, p.wait_limit_ns);
+              if (++stage == C::kStages) stage = 0, parity ^= 1;
             }
           }
+          __syncwarp();
+          break;
         }
-        if (!dead) {
-          const unsigned char* at = ring + stage * C::kUnitBytes;
-          const int tok0 = (unit0 + i) * kUnit;
-          const uint32_t lost = (bad >> (2 * stage)) & 3u;
-          if (lost == 0 && tok0 + kUnit <= len - p.q_len + 1) {
+        const uint32_t at = ring0 + stage * C::kUnitBytes;
+        const int tok0 = (unit0 + i) * kUnit;
+        const uint32_t lost = (bad >> (2 * stage)) & 3u;
+        if (lost == 0 && i < open) {
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k) attend(at + k * C::kTileBytes, tok0 + k * int4::kTile, std::false_type{});
-          } else {
+          for (int k = 0; k < 2; ++k) attend(at + k * C::kTileBytes, tok0 + k * int4::kTile, std::false_type{});
+        } else {
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k)
-              if ((lost >> k & 1u) == 0) attend(at + k * C::kTileBytes, tok0 + k * int4::kTile, std::true_type{});
-          }
+          for (int k = 0; k < 2; ++k)
+            if ((lost >> k & 1u) == 0) attend(at + k * C::kTileBytes, tok0 + k * int4::kTile, std::true_type{});
         }
-        phase ^= 1u << stage;
-        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+        if (++stage == C::kStages) stage = 0, parity ^= 1;
         __syncwarp();  // every lane has read the stage
-        if (!dead) produce();
+        produce();
       }
 
       // ---- end of the piece
@@ -614,8 +654,9 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
             for (int u = 0; u < G; ++u) pm[nt][u][c] += __shfl_xor_sync(0xffffffffu, pm[nt][u][c], d);
           }
       const bool whole = count == n;
-      // only the first piece of a range can be cut and not reach its end; at the end the ring is idle
-      float* rec = rec_of[count < left ? 0 : 1];
+      // only the first piece of a range can be cut and not reach its end
+      const int which = 2 * warp + (count < left ? 0 : 1);
+      float* rec = record(which);
       __syncwarp();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -625,7 +666,9 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           const float inv = l[nt][c] != 0.0f ? 1.0f / l[nt][c] : 0.0f;  // NaN stays NaN
 #pragma unroll
           for (int u = 0; u < G; ++u) {
-            const float even = 0x1p24f / F[nt][c], odd = 0x1p20f / F[nt][c];
+            // 1 / F: a power of two in [2^-126, 2^126]
+            const float over = __uint_as_float((254u << 23) - __float_as_uint(F[nt][c]));
+            const float even = 0x1p24f * over, odd = 0x1p20f * over;
             float y[8];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -653,14 +696,14 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           }
         }
       if (!whole && lane == 0) {
-        Piece& pc = pieces[2 * warp + (rec == rec_of[1])];
-        pc.start = pos - unit0;
+        Piece& pc = pieces[which];
+        pc.start = first;
         pc.units = n;
         pc.b = b;
         pc.seg = seg;
       }
-      pos += count;
-      left -= count;
+      first += n + kSegCost;
+      left -= count + kSegCost;
       unit0 = 0;
       if (left > 0 && ++seg == segs) {
         seg = 0;
@@ -668,115 +711,178 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
       }
     }
   }
+  // Rows of sequences without a token (a length out of range counts as none and is reported).
+  for (int64_t b = me; b < p.num_seqs; b += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int raw = __ldg(p.seq_lens + b);
+    if (checked_len(p, static_cast<int>(b)) != 0) continue;
+    if (raw != 0 && lane == 0) atomicOr(p.err, kErrBounds);
+    uint4* o = reinterpret_cast<uint4*>(p.out + b * p.q_len * p.num_heads * D);
+    for (int i = lane; i < p.q_len * p.num_heads * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+  }
+
   __syncthreads();
 
   // ---- merge what the ranges cut: over the CTA's warps, then over CTAs
-  const int64_t cta_start = start_of(static_cast<int64_t>(blockIdx.x) * kWarps);
-  const int64_t cta_end = start_of(static_cast<int64_t>(blockIdx.x + 1) * kWarps);
-  auto record = [&](int i) {
-    return reinterpret_cast<const float*>((i & 1) ? smem + (i / 2) * C::kRingBytes
-                                                  : smem + kWarps * C::kRingBytes + (i / 2) * C::kRecBytes);
-  };
-  auto out_row = [&](int b, int seg, int r, bool& valid) {
+  const int64_t cta_start = split.start(static_cast<int64_t>(blockIdx.x) * kWarps);
+  const int64_t cta_end = split.start(static_cast<int64_t>(blockIdx.x + 1) * kWarps);
+  auto out_row = [&](int b, int seg, int r) -> uint16_t* {
     const int head = seg / p.n_rt, row = (seg - head * p.n_rt) * C::kRows + r;
-    valid = row < p.rows;
+    if (row >= p.rows) return nullptr;
     const int tok = token_of(p, row);
     return p.out + ((static_cast<int64_t>(b) * p.q_len + tok) * p.num_heads + static_cast<int64_t>(head) * p.group +
                     (row - tok * p.group)) * D;
   };
-  const int64_t slot_floats = C::kRecFloats;
-  int outward[2] = {-1, -1};  // pieces whose segment goes on in another CTA: started before, ends after
-  for (int i = 0; i < 2 * kWarps;) {
-    if (pieces[i].units == 0) {
-      ++i;
-      continue;
+  static_assert(C::kRows <= 4 * kWarps, "a warp has four rows of a segment at most");
+  constexpr int kMl = C::kRows * D;  // (reference, sum) of the rows, behind the rows
+  const int col = 4 * (lane % (D / 4));
+  // Merges rows r0 .. r0 + 3 of a segment's records -- record_of(i), i < count, of the first 16 only
+  // those with bit i of `some` set -- into their output rows, or into the rows of `into`.  Lane i
+  // looks after records i % 16 of 16, rows r0 + i / 16 and two further; four records of four rows are
+  // loaded at a time, since what a merge waits for is the way to L2.
+  auto merge = [&](int b, int seg, int r0, int rows, int count, uint32_t some, auto record_of, auto load2, auto load4, float* into) {
+    float top[2] = {kNone, kNone}, sum[2] = {0.0f, 0.0f};
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int valid = min(4, rows - r0);
+#pragma unroll 1
+    for (int c = 0; c < count; c += 16) {
+      const int i0 = lane & 15;
+      const bool mine = c + i0 < count && (some >> i0 & 1);
+      const float* rec = mine ? record_of(c + i0) : nullptr;
+      float a[2], before[2];
+      float2 ml[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = lane / 16 + 2 * j;
+        ml[j] = make_float2(kNone, 0.0f);
+        if (mine && r < valid) ml[j] = load2(rec + kMl + 2 * (r0 + r));
+      }
+      uint32_t todo = __ballot_sync(0xffffffffu, mine) & 0xffffu;
+      bool weighed = false;
+#pragma unroll 1
+      while (todo) {
+        float4 y[4][4];
+        int from[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          from[q] = todo ? __ffs(todo) - 1 : -1;
+          todo &= todo - 1;
+          const float* at = reinterpret_cast<const float*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rec), max(0, from[q])));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[q][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (from[q] >= 0 && k < valid) y[q][k] = load4(at + (r0 + k) * D + col);
+          }
+        }
+        if (!weighed) {  // (after the first loads are on their way)
+          weighed = true;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float now = fmaxf(top[j], ml[j].x);
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+            before[j] = ptx::ex2(top[j] - now);
+            a[j] = ptx::ex2(ml[j].x - now);
+            top[j] = now;
+            float part = a[j] * ml[j].y;
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+            sum[j] = fmaf(sum[j], before[j], part);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float f = __shfl_sync(0xffffffffu, before[k / 2], 16 * (k % 2));
+            acc[k].x *= f;
+            acc[k].y *= f;
+            acc[k].z *= f;
+            acc[k].w *= f;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float w = __shfl_sync(0xffffffffu, a[k / 2], 16 * (k % 2) + max(0, from[q]));
+            if (from[q] < 0) w = 0.0f;
+            acc[k].x = fmaf(w, y[q][k].x, acc[k].x);
+            acc[k].y = fmaf(w, y[q][k].y, acc[k].y);
+            acc[k].z = fmaf(w, y[q][k].z, acc[k].z);
+            acc[k].w = fmaf(w, y[q][k].w, acc[k].w);
+          }
+      }
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float t = __shfl_sync(0xffffffffu, top[k / 2], 16 * (k % 2));
+      const float l = __shfl_sync(0xffffffffu, sum[k / 2], 16 * (k % 2));
+      if (k < valid) {
+        if (into == nullptr) {
+          if (lane < D / 4) st_bf16x4(out_row(b, seg, r0 + k) + col, acc[k], l != 0.0f ? 1.0f / l : 0.0f);
+        } else {
+          if (lane < D / 4) __stcg(reinterpret_cast<float4*>(into + (r0 + k) * D + col), acc[k]);
+          if (lane == 0) __stcg(reinterpret_cast<float2*>(into + kMl + 2 * (r0 + k)), make_float2(t, l));
+        }
+      }
+    }
+  };
+  // rows of the segment's row tile
+  auto rows_of = [&](int seg) { return min(C::kRows, p.rows - seg % p.n_rt * C::kRows); };
+
+  // over the CTA's warps: lane i looks after piece i; (segment, four rows) go to the warps in turn
+  const int64_t its_start = lane < 2 * kWarps ? pieces[lane].start : 0;
+  uint32_t todo = __ballot_sync(0xffffffffu, lane < 2 * kWarps && pieces[lane & (2 * kWarps - 1)].units != 0);
+  int outward[2] = {-1, -1};  // pieces whose segment started in an earlier CTA; goes on in a later one
+  int turn = 4 * warp;
+#pragma unroll 1
+  while (todo) {
+    const int i = __ffs(todo) - 1;
     const Piece pc = pieces[i];
-    uint32_t mine = 0;  // records of this segment
-    int j = i;
-    for (; j < 2 * kWarps && (pieces[j].units == 0 || pieces[j].start == pc.start); ++j)
-      if (pieces[j].units != 0) mine |= 1u << j;
+    const uint32_t mine = todo & __ballot_sync(0xffffffffu, its_start == pc.start);
+    todo &= ~mine;
     const bool inside = pc.start >= cta_start && pc.start + pc.units <= cta_end;
     const int slot = pc.start < cta_start ? 0 : 1;
     if (!inside) outward[slot] = i;
-    for (int r = warp; r < C::kRows; r += kWarps) {
-      bool valid;
-      uint16_t* dst = out_row(pc.b, pc.seg, r, valid);
-      if (!valid) continue;
-      float top = kNone;
-      for (uint32_t m = mine; m; m &= m - 1) top = fmaxf(top, record(__ffs(m) - 1)[C::kRows * D + 2 * r]);
-      float sum = 0.0f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (uint32_t m = mine; m; m &= m - 1) {
-        const float* rec = record(__ffs(m) - 1);
-        const float a = ptx::ex2(rec[C::kRows * D + 2 * r] - top);
-        sum = fmaf(a, rec[C::kRows * D + 2 * r + 1], sum);
-        if (lane < D / 4) {
-          const float4 y = *reinterpret_cast<const float4*>(rec + r * D + 4 * lane);
-          acc.x = fmaf(a, y.x, acc.x);
-          acc.y = fmaf(a, y.y, acc.y);
-          acc.z = fmaf(a, y.z, acc.z);
-          acc.w = fmaf(a, y.w, acc.w);
-        }
-      }
-      if (inside) {
-        if (lane < D / 4) st_bf16x4(dst + 4 * lane, acc, sum != 0.0f ? 1.0f / sum : 0.0f);
-      } else {
-        float* ws = p.slots + (2 * static_cast<int64_t>(blockIdx.x) + slot) * slot_floats;
-        if (lane < D / 4) __stcg(reinterpret_cast<float4*>(ws + r * D + 4 * lane), acc);
-        if (lane == 0) __stcg(reinterpret_cast<float2*>(ws + C::kRows * D + 2 * r), make_float2(top, sum));
-      }
-    }
-    i = j;
+    float* into = inside ? nullptr : p.slots + (2 * static_cast<int64_t>(blockIdx.x) + slot) * C::kRecFloats;
+#pragma unroll 1
+    for (; turn < C::kRows; turn += 4 * kWarps)
+      if (turn < rows_of(pc.seg))
+        merge(pc.b, pc.seg, turn, rows_of(pc.seg), 2 * kWarps, mine, record,
+              [](const float* x) { return *reinterpret_cast<const float2*>(x); },
+              [](const float* x) { return *reinterpret_cast<const float4*>(x); }, into);
+    turn -= C::kRows;
   }
   if (outward[0] < 0 && outward[1] < 0) return;  // (the same in every thread)
+
+  // over CTAs
   __threadfence();
   __syncthreads();
   if (threadIdx.x < 2) {
-    int last = 0;
+    int2 ctas = make_int2(0, -1);  // empty unless this CTA is the last to arrive
     const int i = outward[threadIdx.x];
     if (i >= 0) {
       const Piece pc = pieces[i];
-      const int first = static_cast<int>(owner_of(pc.start) / kWarps);
-      const int ctas = static_cast<int>(owner_of(pc.start + pc.units - 1) / kWarps) - first + 1;
-      last = atomicAdd(p.counters + first, 1) == ctas - 1;
+      const int from = static_cast<int>(split.owner(pc.start) / kWarps);
+      const int to = static_cast<int>(split.owner(pc.start + pc.units - 1) / kWarps);
+      if (atomicAdd(p.counters + from, 1) == to - from) ctas = make_int2(from, to);
     }
-    last_of[threadIdx.x] = last;
+    last_of[threadIdx.x] = ctas;
   }
   __syncthreads();
+#pragma unroll 1
   for (int k = 0; k < 2; ++k) {
-    if (!last_of[k]) continue;
+    const int from = last_of[k].x, to = last_of[k].y;
+    if (to < from) continue;
     __threadfence();
     const Piece pc = pieces[outward[k]];
-    const int first = static_cast<int>(owner_of(pc.start) / kWarps);
-    const int last = static_cast<int>(owner_of(pc.start + pc.units - 1) / kWarps);
-    if (threadIdx.x == 0) p.counters[first] = 0;
-    for (int r = warp; r < C::kRows; r += kWarps) {
-      bool valid;
-      uint16_t* dst = out_row(pc.b, pc.seg, r, valid);
-      if (!valid) continue;
-      // the first CTA's part is its second slot, the others' their first
-      auto part = [&](int c) { return p.slots + (2 * static_cast<int64_t>(c) + (c == first)) * slot_floats; };
-      float top = kNone;
-      for (int c = first + lane; c <= last; c += 32) top = fmaxf(top, __ldcg(part(c) + C::kRows * D + 2 * r));
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      float sum = 0.0f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int c = first; c <= last; ++c) {
-        const float* ws = part(c);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(ws + C::kRows * D + 2 * r));
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(ws + r * D + 4 * (lane % (D / 4))));
-        const float a = ptx::ex2(ml.x - top);
-        sum = fmaf(a, ml.y, sum);
-        acc.x = fmaf(a, y.x, acc.x);
-        acc.y = fmaf(a, y.y, acc.y);
-        acc.z = fmaf(a, y.z, acc.z);
-        acc.w = fmaf(a, y.w, acc.w);
-      }
-      if (lane < D / 4) st_bf16x4(dst + 4 * lane, acc, sum != 0.0f ? 1.0f / sum : 0.0f);
-    }
+    if (threadIdx.x == 0) p.counters[from] = 0;
+    // the first CTA's part is its second slot, the others' their first
+    auto part = [&](int c) { return p.slots + (2 * static_cast<int64_t>(from + c) + (c == 0)) * C::kRecFloats; };
+    if (4 * warp < rows_of(pc.seg))
+      merge(pc.b, pc.seg, 4 * warp, rows_of(pc.seg), to - from + 1, 0xffffu, part,
+            [](const float* x) { return __ldcg(reinterpret_cast<const float2*>(x)); },
+            [](const float* x) { return __ldcg(reinterpret_cast<const float4*>(x)); }, nullptr);
   }
 }
 
@@ -785,14 +891,22 @@ namespace {
 template <int D, int NT>
 Int4Plan plan_of() {
   using C = Cfg<D, NT>;
-  return {NT, C::kCtas, static_cast<size_t>(C::kSmem), static_cast<size_t>(C::kRecFloats) * 2 * sizeof(float)};
+  return {NT, kWarps, C::kCtas, static_cast<size_t>(C::kSmem), static_cast<size_t>(C::kRecFloats) * (2 + kWarps) * sizeof(float)};
 }
 
 template <int D, int NT>
 cudaError_t launch(const Int4DecodeParams& p, int grid, cudaStream_t stream, bool overlap) {
   const auto kernel = decode_int4_kernel<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NT>::kSmem);
+  // the attribute is kept per device: set by the first call on each
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || (set.load(std::memory_order_relaxed) >> dev & 1) == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NT>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(32 * kWarps);

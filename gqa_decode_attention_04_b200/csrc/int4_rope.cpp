@@ -188,7 +188,7 @@ gqa_status decode(const void* q, const void* kv_pages, const int32_t* block_tabl
   const int64_t tiles = static_cast<int64_t>(num_seqs) * num_kv_heads * n_rt *
                         (static_cast<int64_t>(max_blocks) * (page_size / kTile));
   int64_t grid = knobs.workers > 0 ? knobs.workers : static_cast<int64_t>(sms) * plan.ctas_per_sm;
-  const int64_t limits[] = {fit, gqa::kInt4MaxCtas, (tiles + 7) / 8};
+  const int64_t limits[] = {fit, gqa::kInt4MaxCtas, (tiles + plan.warps - 1) / plan.warps};
   for (const int64_t limit : limits)
     if (grid > limit) grid = limit;
 

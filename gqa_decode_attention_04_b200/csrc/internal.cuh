@@ -149,7 +149,7 @@ struct Int4DecodeParams {
   const int32_t* block_table; // [B, MB]
   const int32_t* seq_lens;    // [B]
   int32_t* counters;          // [kInt4MaxCtas], zero between launches
-  float* slots;               // two per CTA: [rows][D] sums, then [rows][2] (reference, sum)
+  float* slots;               // two per CTA, then one per warp: [rows][D] sums, then [rows][2] (reference, sum)
   uint32_t* err;
   int num_seqs, num_heads, num_kv_heads, group, q_len;
   int rows;                   // query rows per kv head: group * q_len
@@ -164,9 +164,10 @@ struct Int4DecodeParams {
 constexpr int kInt4MaxCtas = 4096;
 struct Int4Plan {
   int n_tiles;        // 8-row MMA tiles of a warp
+  int warps;          // of a CTA
   int ctas_per_sm;
   size_t smem_bytes;
-  size_t slot_bytes;  // of one CTA (two slots)
+  size_t slot_bytes;  // of one CTA
 };
 Int4Plan plan_decode_int4(int head_dim, int rows);
 cudaError_t launch_decode_int4(const Int4DecodeParams& p, const Int4Plan& plan, int head_dim, int grid,
