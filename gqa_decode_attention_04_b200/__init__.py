@@ -567,10 +567,11 @@ class _on:
 
     def __init__(self, dev, stream):
         index = dev.index
-        if stream is None and index == _current_device():
-            self.ptr, self.guards = _current_stream(index), None
-        elif stream is None:
-            self.ptr, self.guards = _current_stream(index), (torch.cuda.device(dev),)
+        self.guards = None
+        if stream is None:
+            self.ptr = _current_stream(index)
+            if index != _current_device():
+                self.guards = (torch.cuda.device(dev),)
         else:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=dev)
@@ -589,42 +590,46 @@ class _on:
         return False
 
 
-def _current_device() -> int:
-    return torch.cuda.current_device()
+_current_device = torch.cuda.current_device
 
 
 def _current_stream(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 
 
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same, 2 us sooner: as torch's own launchers ask
-    _current_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _is(t, dtype, dev) -> bool:
-    """_need's conditions, without its messages: the calls below ask this first."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev.index
-            and t.is_contiguous())
+# the same two without a Stream object in between (3 us less a call), where this torch has them
+_current_device = getattr(torch._C, "_cuda_getDevice", _current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 def _all(dev, *wanted) -> None:
-    """(tensor, name, dtype) triples that _need is to hold for."""
+    """_need for (tensor, name, dtype) triples; its conditions are asked first, its messages made only if
+    one does not hold."""
+    index = dev.index
     for t, name, dtype in wanted:
-        if not _is(t, dtype, dev):
-            _need(t, name, dtype, dev)
+        try:
+            if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
+        _need(t, name, dtype, dev)
 
 
 def _need_rows(t, name, heads, dim, tokens, dev):
     """bf16 rows [tokens, heads, dim], contiguous but for the stride between tokens, which is returned
     (in elements).  heads, tokens None: any."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda and t.get_device() == dev.index):
+    try:
+        here = t.dtype is torch.bfloat16 and t.get_device() == dev.index
+    except AttributeError:
+        here = False
+    if not here:
         _need(t.contiguous() if isinstance(t, torch.Tensor) else t, name, torch.bfloat16, dev)
     shape = t.shape
     if (len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads)
             or (tokens is not None and shape[0] != tokens)):
         raise ValueError(f"{name} must be [num_tokens, heads, head_dim] = [{tokens or 'T'}, {heads or 'H'}, {dim}], "
                          f"got {list(shape)}")
-    if t.is_contiguous() or 0 in shape:
+    if t.is_contiguous():
         return shape[1] * dim
     stride = t.stride()
     if stride[2] != 1 or (shape[1] > 1 and stride[1] != dim):
@@ -632,36 +637,35 @@ def _need_rows(t, name, heads, dim, tokens, dev):
     return stride[0] if shape[0] > 1 else shape[1] * dim
 
 
-def _rope(fn, q, k_new, v_new, cos_sin, pools, scales, block_table, positions, seq_ids, interleaved, q_out, stream,
+def _rope(fn, q, k_new, v_new, cos_sin, pools, block_table, positions, seq_ids, interleaved, q_out, stream, dev,
           pool_shape):
-    dev = pools[0].device
+    """fn on the pools (and scales) whose addresses `pools` holds."""
     P, Hk, ps, D = pool_shape
     q_stride = _need_rows(q, "q", None, D, None, dev)
-    T, H, _ = q.shape
+    T, H, _ = shape = q.shape
     k_stride = _need_rows(k_new, "k_new", Hk, D, T, dev)
     v_stride = _need_rows(v_new, "v_new", Hk, D, T, dev)
     _all(dev, (cos_sin, "cos_sin", torch.float32), (block_table, "block_table", torch.int32),
          (positions, "positions", torch.int32))
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [max_positions, rotary_dim]")
-    if block_table.dim() != 2 or positions.dim() != 1 or positions.shape[0] != T:
-        raise ValueError("block_table must be [num_seqs, max_blocks], positions [num_tokens]")
+    if cos_sin.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("cos_sin must be [max_positions, rotary_dim], block_table [num_seqs, max_blocks]")
+    if positions.shape != shape[:1]:
+        raise ValueError("positions must be [num_tokens]")
     seqs, blocks = block_table.shape
     ids = None
     if seq_ids is not None:
         _all(dev, (seq_ids, "seq_ids", torch.int32))
-        if seq_ids.dim() != 1 or seq_ids.shape[0] != T:
+        if seq_ids.shape != shape[:1]:
             raise ValueError("seq_ids must be [num_tokens]")
         ids = seq_ids.data_ptr()
     elif seqs != T:
         raise ValueError("without seq_ids, token t is sequence t: block_table must have num_tokens rows")
     max_positions, rotary = cos_sin.shape
     with _on(dev, stream) as ptr:
-        q_out = _out(q_out, (T, H, D), dev)
-        _check(fn(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), cos_sin.data_ptr(), q_out.data_ptr(),
-                  *(t.data_ptr() for t in (*pools, *scales)), block_table.data_ptr(), positions.data_ptr(), ids, T, seqs,
-                  H, Hk, D, rotary, 1 if interleaved else 0, max_positions, q_stride, k_stride, v_stride, ps, blocks, P,
-                  ptr))
+        q_out = _out(q_out, shape, dev)
+        _check(fn(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), cos_sin.data_ptr(), q_out.data_ptr(), *pools,
+                  block_table.data_ptr(), positions.data_ptr(), ids, T, seqs, H, Hk, D, rotary, 1 if interleaved else 0,
+                  max_positions, q_stride, k_stride, v_stride, ps, blocks, P, ptr))
     return q_out
 
 
@@ -689,8 +693,9 @@ def rope_kv_append(q, k_new, v_new, cos_sin, k_pages, v_pages, block_table, posi
     _all(dev, (k_pages, "k_pages", torch.bfloat16), (v_pages, "v_pages", torch.bfloat16))
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("page pools must both be [num_pages, num_kv_heads, page_size, head_dim]")
-    return _rope(load_library().gqa_rope_kv_append, q, k_new, v_new, cos_sin, (k_pages, v_pages), (), block_table,
-                 positions, seq_ids, interleaved, q_out, stream, k_pages.shape)
+    return _rope(load_library().gqa_rope_kv_append, q, k_new, v_new, cos_sin,
+                 (k_pages.data_ptr(), v_pages.data_ptr()), block_table, positions, seq_ids, interleaved, q_out, stream,
+                 dev, k_pages.shape)
 
 
 def rope_kv_append_fp8(q, k_new, v_new, cos_sin, k_pages, v_pages, k_scales, v_scales, block_table, positions,
@@ -698,9 +703,16 @@ def rope_kv_append_fp8(q, k_new, v_new, cos_sin, k_pages, v_pages, k_scales, v_s
                        q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rope_kv_append into e4m3 pools (the fp32 rotated k and v, divided by their scales)."""
     dev = k_pages.device
-    shape = _pools_fp8(k_pages, v_pages, k_scales, v_scales, dev)
-    return _rope(load_library().gqa_rope_kv_append_fp8, q, k_new, v_new, cos_sin, (k_pages, v_pages),
-                 (k_scales, v_scales), block_table, positions, seq_ids, interleaved, q_out, stream, shape)
+    _all(dev, (k_pages, "k_pages", torch.uint8), (v_pages, "v_pages", torch.uint8),
+         (k_scales, "k_scales", torch.float32), (v_scales, "v_scales", torch.float32))
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
+        raise ValueError("e4m3 pools must both be [num_pages, num_kv_heads, page_size, head_dim] uint8")
+    if k_scales.shape != shape[1:2] or v_scales.shape != shape[1:2]:
+        raise ValueError("k_scales / v_scales must be [num_kv_heads] float32")
+    return _rope(load_library().gqa_rope_kv_append_fp8, q, k_new, v_new, cos_sin,
+                 (k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr()), block_table,
+                 positions, seq_ids, interleaved, q_out, stream, dev, shape)
 
 
 def _pool_int4(kv_pages, dev):
@@ -715,9 +727,10 @@ def rope_kv_append_int4(q, k_new, v_new, cos_sin, kv_pages, block_table, positio
                         seq_ids: Optional[torch.Tensor] = None, interleaved: bool = False,
                         q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rope_kv_append into a 4-bit pool."""
-    shape = _pool_int4(kv_pages, kv_pages.device)
-    return _rope(load_library().gqa_rope_kv_append_int4, q, k_new, v_new, cos_sin, (kv_pages,), (), block_table,
-                 positions, seq_ids, interleaved, q_out, stream, shape)
+    dev = kv_pages.device
+    shape = _pool_int4(kv_pages, dev)
+    return _rope(load_library().gqa_rope_kv_append_int4, q, k_new, v_new, cos_sin, (kv_pages.data_ptr(),), block_table,
+                 positions, seq_ids, interleaved, q_out, stream, dev, shape)
 
 
 def quantize_pages_int4(k_pages, v_pages, kv_pages: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
