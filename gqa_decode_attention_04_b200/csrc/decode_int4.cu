@@ -481,15 +481,12 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
             }
           }
         // ---- weights; the reference moves only when a score passes it by 12 (in units of log2)
+        // (not in packed pairs: the compiler may contract a packed product and difference, and a score
+        // has to be the same number here and where the reference is taken from it)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint64_t hh = ptx::f2_pack(h[nt][0], h[nt][1]);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint64_t y = ptx::f2_mul(ptx::f2_pack(sc[nt][2 * r], sc[nt][2 * r + 1]), hh);
-            ptx::f2_unpack(y, sc[nt][2 * r], sc[nt][2 * r + 1]);
-          }
-        }
+          for (int x = 0; x < 4; ++x) sc[nt][x] = __fmul_rn(sc[nt][x], h[nt][x % 2]);
         float pr[NT][4], w[NT][G][4];
         bool up;
         auto weigh = [&]() {

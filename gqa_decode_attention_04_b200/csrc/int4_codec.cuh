@@ -54,48 +54,76 @@ __device__ __forceinline__ float bf16_round(float x) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
 
-// Codes of this lane's 8 channels (nibble n = channel n) of a group held by 8 aligned lanes;
-// pair = step (low half) | low (high half), the same in the 8 lanes.  Every lane of the warp
-// takes part.  The quotient (x - low) / step is the correctly rounded one: with
-// r = RN(1 / step), y = RN(t r) and the exact residual e = t - y step (one fma), RN(y + e r)
-// is RN(t / step) (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990) where nothing over- or underflows; a step outside
-// [2^-60, 2^60] takes the plain division.  A tie of code + 1/2 is therefore decided as in
-// exact arithmetic, to the even code.
-__device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t& pair) {
+// Codes of this lane's 8 W channels (nibble n of words[w] = channel 8 w + n) of a group held by
+// 8 / W aligned lanes; pair = step (low half) | low (high half), the same in those lanes.  Every
+// lane of the warp takes part.
+//
+// Both quotients, range / 15 and (x - low) / step, are the correctly rounded ones: with r = RN(1 / d),
+// y = RN(a r) and the exact residual e = a - y d (one fma), RN(y + e r) is RN(a / d) (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990) where nothing
+// over- or underflows; a warp with a range outside [2^-60, 2^60] takes plain divisions.  A tie of
+// code + 1/2 is therefore decided as in exact arithmetic, to the even code.  The arithmetic is what
+// bounds the writers (a pool of 150 MB: 28 us for its bytes), so it goes in packed pairs, and the
+// codes are put together as one exact number, c0 + 16 c1 + 256 c2 + 4096 c3.
+template <int W>
+__device__ __forceinline__ void quantize(const float (&x)[8 * W], uint32_t (&words)[W], uint32_t& pair) {
   float lo = x[0], hi = x[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
+  for (int i = 1; i < 8 * W; ++i) {
     lo = min_nan(lo, x[i]);
     hi = max_nan(hi, x[i]);
   }
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1) {
+  for (int d = 1; d < 8 / W; d <<= 1) {
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, d));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, d));
   }
   const float low = bf16_round(lo);
-  const float step = bf16_round(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-  if (!(fabsf(low) < INFINITY) || !(step < INFINITY)) {  // a NaN, an infinity, or an infinite range
-    pair = 0x7fff7fffu;
-    return 0;
-  }
-  pair = __float_as_uint(low) | (__float_as_uint(step) >> 16);
-  if (step == 0.0f) return 0;
-  const float r = __frcp_rn(step);
-  const bool plain = step < 0x1p-60f || step > 0x1p60f;
-  uint32_t word = 0;
+  const float range = __fsub_rn(hi, lo);
+  const bool usual = range >= 0x1p-60f && range <= 0x1p60f && fabsf(low) < INFINITY;
+  if (__all_sync(0xffffffffu, usual)) {
+    constexpr float kFifteenth = 1.0f / 15.0f;
+    float step = __fmul_rn(range, kFifteenth);
+    step = bf16_round(__fmaf_rn(__fmaf_rn(-step, 15.0f, range), kFifteenth, step));
+    pair = __float_as_uint(low) | (__float_as_uint(step) >> 16);
+    const float r = __frcp_rn(step);
+    const uint64_t r2 = ptx::f2_pack(r, r), step2 = ptx::f2_pack(-step, -step), low2 = ptx::f2_pack(low, low);
+    const uint64_t up2 = ptx::f2_pack(12582912.0f, 12582912.0f);  // 1.5 * 2^23: adding it rounds to a whole number
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float t = __fsub_rn(x[i], low);
-    float y = __fmul_rn(t, r);
-    y = __fmaf_rn(__fmaf_rn(-y, step, t), r, y);
-    if (plain) y = __fdiv_rn(t, step);
-    y = fminf(fmaxf(y, 0.0f), 15.0f);
-    // adding 1.5 * 2^23 leaves rint(y), ties to even, in the low mantissa bits
-    word = (word << 4) | (__float_as_uint(__fadd_rn(y, 12582912.0f)) & 15u);
+    for (int w = 0; w < W; ++w) {
+      float c[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t t = ptx::f2_sub(ptx::f2_pack(x[8 * w + 2 * i], x[8 * w + 2 * i + 1]), low2);
+        uint64_t y = ptx::f2_mul(t, r2);
+        y = ptx::f2_fma(ptx::f2_fma(y, step2, t), r2, y);
+        float a, b;
+        ptx::f2_unpack(y, a, b);
+        a = fminf(fmaxf(a, 0.0f), 15.0f);
+        b = fminf(fmaxf(b, 0.0f), 15.0f);
+        ptx::f2_unpack(ptx::f2_sub(ptx::f2_add(ptx::f2_pack(a, b), up2), up2), c[2 * i], c[2 * i + 1]);
+      }
+      float half[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        half[i] = fmaf(4096.0f, c[4 * i + 3], fmaf(256.0f, c[4 * i + 2], fmaf(16.0f, c[4 * i + 1], c[4 * i])));
+      // 2^23 + n has the whole number n in its low mantissa bits
+      words[w] = __byte_perm(__float_as_uint(half[0] + 8388608.0f), __float_as_uint(half[1] + 8388608.0f), 0x5410);
+    }
+    return;
   }
-  return word;
+  const float step = bf16_round(__fdiv_rn(range, 15.0f));
+  const bool finite = fabsf(low) < INFINITY && step < INFINITY;  // else a NaN, an infinity, or an infinite range
+  pair = finite ? __float_as_uint(low) | (__float_as_uint(step) >> 16) : 0x7fff7fffu;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    words[w] = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+      const float y = finite && step > 0.0f ? __fdiv_rn(__fsub_rn(x[8 * w + i], low), step) : 0.0f;
+      words[w] = (words[w] << 4) | static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(y, 0.0f), 15.0f)));
+    }
+  }
 }
 
 // bf16 pairs (element 0 in the low half) of 16 bytes as 8 floats.

@@ -131,7 +131,10 @@ struct RopeAppendParams {
   int num_tokens, num_seqs, num_heads, num_kv_heads;
   int rotary_dim;             // 0: nothing is rotated
   int interleaved, max_positions, page_size, max_blocks, num_pages;
-  int chunks;                 // blocks per token (set by the launcher)
+  // set by the launcher: blocks per token, or rows of a token side by side; division by page_size
+  int chunks, spread_log2;
+  uint32_t ps_magic;
+  int ps_shift;
 };
 cudaError_t launch_rope_append(const RopeAppendParams& p, int cache, int head_dim, int sms, cudaStream_t stream);
 

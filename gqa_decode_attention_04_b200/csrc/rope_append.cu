@@ -6,7 +6,9 @@
 // token) is held by head_dim / 8 lanes of 16 bytes each.  In the half-split style the partner
 // of a channel lies rotary_dim / 16 lanes away: the pair is brought together by shuffles of
 // the packed bf16 words, so no element is read twice.  A thread keeps its cos and sin for all
-// the rows it handles (the same channels of up to kRows heads of one token).
+// the rows it handles (the same channels of several heads of one token).
+#include <climits>
+
 #include <cuda_fp8.h>
 
 #include "int4_codec.cuh"
@@ -18,6 +20,11 @@ namespace gqa {
 namespace {
 
 constexpr int kThreads = 256;
+// Rows of a thread whose loads are in flight together, and blocks per SM that the registers are
+// held down for: 16384 tokens of 64 + 16 heads into 4 bits with the pool read back take 182 us with
+// (4, 4), 206 with (4, 3), 191 with (4, 5), 201 with (3, 4); 5987 tokens of 12 + 4 heads into e4m3
+// 6.3, 6.0, 8.4, 6.6 us.
+constexpr int kBatch = 4, kBlocks = 4;
 
 __device__ __forceinline__ uint32_t codes2(float a, float b, float s) {
   return static_cast<uint32_t>(
@@ -26,136 +33,176 @@ __device__ __forceinline__ uint32_t codes2(float a, float b, float s) {
 
 }  // namespace
 
-// One block: up to kRows * kThreads / (D / 8) rows of one token.  Rows are the q heads, then
-// the k heads, then the v heads.
-template <int D, int CACHE, int kRows>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendParams p) {
+// A token's rows are the q heads, then the k heads, then the v heads.  MANY: 1 << p.spread_log2 q rows
+// of a token are worked on side by side, each thread going on to every such-manieth, and likewise its
+// k and v rows.  Otherwise one row a thread, p.chunks blocks per token.
+template <int D, int CACHE, bool MANY>
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const RopeAppendParams p) {
   // A decode launched right after this one may start its prologue; it waits for this grid
   // before it reads anything that is written here.
   ptx::pdl_launch_dependents();
   constexpr int kLanes = D / 8;
-  constexpr int kSlots = kThreads / kLanes;  // rows in flight
-  const int t = blockIdx.x / p.chunks;
-  const int first_row = (blockIdx.x - t * p.chunks) * (kSlots * kRows);
+  constexpr int kSlots = kThreads / kLanes;  // rows in flight in a block
   const int j = threadIdx.x % kLanes;
   const int slot = threadIdx.x / kLanes;
-
-  const int s = p.seq_ids != nullptr ? __ldg(p.seq_ids + t) : t;
-  if (s < 0) return;  // padding
-  const int pos = __ldg(p.positions + t);
-  int page = -1;
-  if (s < p.num_seqs && pos >= 0 && pos < p.max_positions &&
-      static_cast<int64_t>(pos) < static_cast<int64_t>(p.max_blocks) * p.page_size)
-    page = __ldg(p.block_table + static_cast<int64_t>(s) * p.max_blocks + pos / p.page_size);
-  if (page < 0 || page >= p.num_pages) {
-    if (first_row == 0 && threadIdx.x == 0) atomicOr(p.err, kErrBounds);
-    return;
+  int t, row, stride;
+  if (MANY) {
+    t = blockIdx.x * (kSlots >> p.spread_log2) + (slot >> p.spread_log2);
+    stride = 1 << p.spread_log2;
+    row = slot & (stride - 1);
+  } else {
+    t = blockIdx.x / p.chunks;
+    row = (blockIdx.x - t * p.chunks) * kSlots + slot;
+    stride = INT_MAX / 2;
   }
-  const int in_page = pos % p.page_size;
+  // (a warp may hold rows of several tokens, of which some are skipped: all its lanes stay for the shuffles)
+  bool live = t < p.num_tokens;
+  const int s = !live ? -1 : (p.seq_ids != nullptr ? __ldg(p.seq_ids + t) : t);
+  const int pos = live ? __ldg(p.positions + t) : 0;
+  live = s >= 0;  // else padding
+  int page = -1, in_page = 0;
+  if (live) {
+    if (s < p.num_seqs && pos >= 0 && pos < p.max_positions &&
+        static_cast<int64_t>(pos) < static_cast<int64_t>(p.max_blocks) * p.page_size) {
+      const int block = p.page_size == 1 ? pos : fast_div(pos, p.ps_magic, p.ps_shift);
+      in_page = pos - block * p.page_size;
+      page = __ldg(p.block_table + static_cast<int64_t>(s) * p.max_blocks + block);
+    }
+    if (page < 0 || page >= p.num_pages) {
+      live = false;
+      if (row == 0 && j == 0) atomicOr(p.err, kErrBounds);
+    }
+  }
 
   const int half_lanes = p.rotary_dim / 16;  // lanes of the first half of the rotated channels
   const bool rotated = j < 2 * half_lanes;
+  const bool second = !p.interleaved && j >= half_lanes;
+  // x[i] becomes x[i] c[i] + (its partner) sn[i], the sine's sign taken in; (1, 0) where nothing turns
   float c[8], sn[8];
-  if (rotated) {
-    const float* row = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) c[m] = 1.0f, sn[m] = 0.0f;
+  if (rotated && live) {
+    const float* at = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim;
     if (p.interleaved) {  // pairs (2 m, 2 m + 1), m = 4 j .. 4 j + 3
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row) + j);
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row + p.rotary_dim / 2) + j);
-      c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
-      sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
+      const float4 a = __ldg(reinterpret_cast<const float4*>(at) + j);
+      const float4 b = __ldg(reinterpret_cast<const float4*>(at + p.rotary_dim / 2) + j);
+      c[0] = c[1] = a.x; c[2] = c[3] = a.y; c[4] = c[5] = a.z; c[6] = c[7] = a.w;
+      sn[0] = -b.x; sn[1] = b.x; sn[2] = -b.y; sn[3] = b.y; sn[4] = -b.z; sn[5] = b.z; sn[6] = -b.w; sn[7] = b.w;
     } else {
-      const int i = 8 * (j < half_lanes ? j : j - half_lanes);
+      const int i = 8 * (second ? j - half_lanes : j);
+      const float sign = second ? 1.0f : -1.0f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(row + i) + h);
-        const float4 b = __ldg(reinterpret_cast<const float4*>(row + p.rotary_dim / 2 + i) + h);
+        const float4 a = __ldg(reinterpret_cast<const float4*>(at + i) + h);
+        const float4 b = __ldg(reinterpret_cast<const float4*>(at + p.rotary_dim / 2 + i) + h);
         c[4 * h] = a.x; c[4 * h + 1] = a.y; c[4 * h + 2] = a.z; c[4 * h + 3] = a.w;
-        sn[4 * h] = b.x; sn[4 * h + 1] = b.y; sn[4 * h + 2] = b.z; sn[4 * h + 3] = b.w;
+        sn[4 * h] = sign * b.x; sn[4 * h + 1] = sign * b.y; sn[4 * h + 2] = sign * b.z; sn[4 * h + 3] = sign * b.w;
       }
     }
   }
-  const bool second = !p.interleaved && j >= half_lanes;
   // the lane that holds the other half of this lane's pairs (itself where nothing is exchanged)
   const int lane = threadIdx.x & 31;
   const int partner = p.interleaved || !rotated ? lane : (second ? lane - half_lanes : lane + half_lanes);
-
-  const int rows = p.num_heads + 2 * p.num_kv_heads;
-  uint4 in[kRows];
+  auto rotate = [&](const uint4 in, float (&x)[8]) {
+    int4::unpack8(in, x);
+    float y[8];
+    if (p.interleaved) {
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int row = first_row + k * kSlots + slot;
-    in[k] = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const uint16_t* src;
-      if (row < p.num_heads) {
-        src = p.q + t * p.q_stride + static_cast<int64_t>(row) * D;
-      } else if (row < p.num_heads + p.num_kv_heads) {
-        src = p.k + t * p.k_stride + static_cast<int64_t>(row - p.num_heads) * D;
-      } else {
-        src = p.v + t * p.v_stride + static_cast<int64_t>(row - p.num_heads - p.num_kv_heads) * D;
-      }
-      in[k] = *(reinterpret_cast<const uint4*>(src) + j);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int row = first_row + k * kSlots + slot;
-    const bool is_v = row >= p.num_heads + p.num_kv_heads;
-    float x[8];
-    int4::unpack8(in[k], x);
-    uint4 other;
-    other.x = __shfl_sync(0xffffffffu, in[k].x, partner);
-    other.y = __shfl_sync(0xffffffffu, in[k].y, partner);
-    other.z = __shfl_sync(0xffffffffu, in[k].z, partner);
-    other.w = __shfl_sync(0xffffffffu, in[k].w, partner);
-    if (rotated && !is_v) {
-      if (p.interleaved) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float a = x[2 * m], b = x[2 * m + 1];
-          x[2 * m] = __fsub_rn(__fmul_rn(a, c[m]), __fmul_rn(b, sn[m]));
-          x[2 * m + 1] = __fadd_rn(__fmul_rn(b, c[m]), __fmul_rn(a, sn[m]));
-        }
-      } else {
-        float y[8];
-        int4::unpack8(other, y);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          const float ys = __fmul_rn(y[m], sn[m]);
-          x[m] = second ? __fadd_rn(__fmul_rn(x[m], c[m]), ys) : __fsub_rn(__fmul_rn(x[m], c[m]), ys);
-        }
-      }
-    }
-    uint32_t pair = 0, word = 0;
-    // (the whole warp quantises if any of its rows is a cache row, so that the shuffles are whole)
-    if (CACHE == kCacheInt4 && __any_sync(0xffffffffu, row >= p.num_heads && row < rows))
-      word = int4::quantize8(x, pair);
-    if (row >= rows) continue;
-    if (row < p.num_heads) {
-      *(reinterpret_cast<uint4*>(p.q_out + (static_cast<int64_t>(t) * p.num_heads + row) * D) + j) = int4::pack8(x);
-      continue;
-    }
-    const int h = row - p.num_heads - (is_v ? p.num_kv_heads : 0);
-    const int64_t page_head = static_cast<int64_t>(page) * p.num_kv_heads + h;
-    if (CACHE == kCacheInt4) {
-      using L = int4::Layout<D>;
-      uint8_t* tile = p.k_pages + (page_head * (p.page_size / int4::kTile) + in_page / int4::kTile) * L::kTileBytes;
-      const int tau = in_page % int4::kTile;
-      *reinterpret_cast<uint32_t*>(tile + (is_v ? L::v_word(tau, j) : L::k_word(tau, j))) = word;
-      if (j % 8 == 0) *reinterpret_cast<uint32_t*>(tile + L::param(tau, is_v, j / 8)) = pair;
+      for (int m = 0; m < 8; ++m) y[m] = x[m ^ 1];
     } else {
-      const int64_t at = (page_head * p.page_size + in_page) * kLanes + j;
-      uint8_t* pool = is_v ? p.v_pages : p.k_pages;
-      if (CACHE == kCacheBf16) {
-        *(reinterpret_cast<uint4*>(pool) + at) = is_v ? in[k] : int4::pack8(x);
-      } else {
-        const float sc = __ldg((is_v ? p.v_scales : p.k_scales) + h);
-        uint2 w;
-        w.x = codes2(x[0], x[1], sc) | (codes2(x[2], x[3], sc) << 16);
-        w.y = codes2(x[4], x[5], sc) | (codes2(x[6], x[7], sc) << 16);
-        *(reinterpret_cast<uint2*>(pool) + at) = w;
+      uint4 other;
+      other.x = __shfl_sync(0xffffffffu, in.x, partner);
+      other.y = __shfl_sync(0xffffffffu, in.y, partner);
+      other.z = __shfl_sync(0xffffffffu, in.z, partner);
+      other.w = __shfl_sync(0xffffffffu, in.w, partner);
+      int4::unpack8(other, y);
+    }
+    if (rotated) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        // Each product and the sum are rounded, never one fma: the products in packed pairs, the sums
+        // not, which the compiler does not contract (it does contract a packed product and sum).
+        float a[2], b[2];
+        ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(x[2 * m], x[2 * m + 1]), ptx::f2_pack(c[2 * m], c[2 * m + 1])), a[0], a[1]);
+        ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(y[2 * m], y[2 * m + 1]), ptx::f2_pack(sn[2 * m], sn[2 * m + 1])), b[0], b[1]);
+        x[2 * m] = __fadd_rn(a[0], b[0]);
+        x[2 * m + 1] = __fadd_rn(a[1], b[1]);
       }
     }
+  };
+
+  // ---- q
+  const uint4* q_in = reinterpret_cast<const uint4*>(p.q + t * p.q_stride) + j;
+  uint4* q_out = reinterpret_cast<uint4*>(p.q_out + static_cast<int64_t>(t) * p.num_heads * D) + j;
+  constexpr int kQ = MANY ? kBatch : 1;
+#pragma unroll 1
+  for (int r0 = row; __any_sync(0xffffffffu, r0 < p.num_heads); r0 += kQ * stride) {
+    uint4 in[kQ];
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) {
+      in[k] = make_uint4(0, 0, 0, 0);
+      if (live && r0 + k * stride < p.num_heads) in[k] = q_in[(r0 + k * stride) * kLanes];
+    }
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) {
+      float x[8];
+      rotate(in[k], x);
+      if (live && r0 + k * stride < p.num_heads) q_out[(r0 + k * stride) * kLanes] = int4::pack8(x);
+    }
+    if (!MANY) break;
+  }
+
+  // ---- k, then v
+  const int cached = 2 * p.num_kv_heads;
+  constexpr int kC = MANY ? 2 : 1;
+#pragma unroll 1
+  for (int r0 = MANY ? row : row - p.num_heads; __any_sync(0xffffffffu, r0 >= 0 && r0 < cached); r0 += kC * stride) {
+    uint4 in[kC];
+#pragma unroll
+    for (int k = 0; k < kC; ++k) {
+      const int r = r0 + k * stride;
+      in[k] = make_uint4(0, 0, 0, 0);
+      if (live && r >= 0 && r < cached) {
+        const uint16_t* src = r < p.num_kv_heads ? p.k + t * p.k_stride + r * D : p.v + t * p.v_stride + (r - p.num_kv_heads) * D;
+        in[k] = *(reinterpret_cast<const uint4*>(src) + j);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kC; ++k) {
+      const int r = r0 + k * stride;
+      if (kC > 1 && !__any_sync(0xffffffffu, r < cached)) break;
+      const bool is_v = r >= p.num_kv_heads;
+      float x[8], turned[8];
+      int4::unpack8(in[k], x);
+      rotate(in[k], turned);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) x[m] = is_v ? x[m] : turned[m];
+      uint32_t pair = 0, word[1] = {0};
+      if (CACHE == kCacheInt4) int4::quantize<1>(x, word, pair);  // (by the whole warp: it shuffles)
+      if (!live || r < 0 || r >= cached) continue;
+      const int h = r - (is_v ? p.num_kv_heads : 0);
+      const int64_t page_head = static_cast<int64_t>(page) * p.num_kv_heads + h;
+      if (CACHE == kCacheInt4) {
+        using L = int4::Layout<D>;
+        uint8_t* tile = p.k_pages + (page_head * (p.page_size / int4::kTile) + in_page / int4::kTile) * L::kTileBytes;
+        const int tau = in_page % int4::kTile;
+        *reinterpret_cast<uint32_t*>(tile + (is_v ? L::v_word(tau, j) : L::k_word(tau, j))) = word[0];
+        if (j % 8 == 0) *reinterpret_cast<uint32_t*>(tile + L::param(tau, is_v, j / 8)) = pair;
+      } else {
+        const int64_t at = (page_head * p.page_size + in_page) * kLanes + j;
+        uint8_t* pool = is_v ? p.v_pages : p.k_pages;
+        if (CACHE == kCacheBf16) {
+          *(reinterpret_cast<uint4*>(pool) + at) = is_v ? in[k] : int4::pack8(x);
+        } else {
+          const float sc = __ldg((is_v ? p.v_scales : p.k_scales) + h);
+          uint2 w;
+          w.x = codes2(x[0], x[1], sc) | (codes2(x[2], x[3], sc) << 16);
+          w.y = codes2(x[4], x[5], sc) | (codes2(x[6], x[7], sc) << 16);
+          *(reinterpret_cast<uint2*>(pool) + at) = w;
+        }
+      }
+    }
+    if (!MANY) break;
   }
 }
 
@@ -165,20 +212,27 @@ template <int D, int CACHE>
 cudaError_t launch_rows(RopeAppendParams p, int sms, cudaStream_t stream) {
   const int rows = p.num_heads + 2 * p.num_kv_heads;
   constexpr int kSlots = kThreads / (D / 8);
-  constexpr int kMany = 4;
-  // Few tokens: one row per thread, so that the call's loads are all in flight at once on as
-  // many SMs as there are rows.  Many: kMany rows per thread, which reads cos and sin once for
-  // all of them.
-  const int64_t chunks1 = (rows + kSlots - 1) / kSlots;
-  const bool many = rows > kSlots && p.num_tokens * chunks1 > int64_t{8} * sms;
-  const int per = many ? kSlots * kMany : kSlots;
-  p.chunks = (rows + per - 1) / per;
-  const int64_t blocks = static_cast<int64_t>(p.num_tokens) * p.chunks;
+  if (p.page_size > 1) divisor_magic(static_cast<uint32_t>(p.page_size), &p.ps_magic, &p.ps_shift);
+  // As long as all rows fit on the GPU at once, one row a thread: the call's loads are all in flight
+  // together.  Beyond that kBatch q rows a thread or more, which finds the token's place, cos and sin once
+  // for all of them.
+  const int64_t per_gpu = int64_t{2048} * sms / (D / 8);
+  int64_t blocks;
+  const bool many = rows > 1 && p.num_tokens * static_cast<int64_t>(rows) > per_gpu;
+  if (many) {
+    p.spread_log2 = 0;
+    while ((2 << p.spread_log2) <= kSlots && (2 << p.spread_log2) * kBatch <= p.num_heads) ++p.spread_log2;
+    const int tokens = kSlots >> p.spread_log2;
+    blocks = (static_cast<int64_t>(p.num_tokens) + tokens - 1) / tokens;
+  } else {
+    p.chunks = (rows + kSlots - 1) / kSlots;
+    blocks = static_cast<int64_t>(p.num_tokens) * p.chunks;
+  }
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (many)
-    rope_append_kernel<D, CACHE, kMany><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    rope_append_kernel<D, CACHE, true><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
   else
-    rope_append_kernel<D, CACHE, 1><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    rope_append_kernel<D, CACHE, false><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -222,19 +222,22 @@ def test_bad_lengths_and_pages_are_skipped_and_reported(cuda_device):
     bt, pages = make_table(rng, lens, 16)
     pool = make_pool(rng, pages, 2, 16, 64)
     q = bf16(rng.standard_normal((4, 8, 64)))
-    good = gq.paged_decode_attn_int4(*device(cuda_device, q, pool, bt, np.array(lens, np.int32)))
+    def fine(out, rows):  # (how a sequence is split depends on the others' lengths: equal within the bound)
+        check(out[rows], q[rows], pool, bt[rows], [lens[b] for b in rows], 0.125)
+
     sl = np.array([40, -5, bt.shape[1] * 16 + 1, 33], np.int32)
     out = gq.paged_decode_attn_int4(*device(cuda_device, q, pool, bt, sl))
     with pytest.raises(gq.GQAError) as e:
         gq.check_device_error()
     assert e.value.status == -4
-    assert torch.equal(out[[0, 3]], good[[0, 3]]) and torch.count_nonzero(out[1:3]) == 0
+    fine(out, [0, 3])
+    assert torch.count_nonzero(out[1:3]) == 0
     bt2 = bt.copy()
     bt2[1, 1], bt2[3, 0] = pages, -7
     out = gq.paged_decode_attn_int4(*device(cuda_device, q, pool, bt2, np.array(lens, np.int32)))
     with pytest.raises(gq.GQAError):
         gq.check_device_error()
-    assert torch.equal(out[[0, 2]], good[[0, 2]])
+    fine(out, [0, 2])
     assert torch.isfinite(out).all()
     gq.check_device_error()
 
