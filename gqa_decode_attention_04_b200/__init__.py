@@ -117,6 +117,22 @@ def library_path() -> str:
 
 
 _lib = None
+_fast = None       # csrc/fastcall.cc: some calls without ctypes, where their outputs are given
+_entry = {}        # addresses of the entry points that it calls
+
+
+def _load_fast(lib) -> None:
+    """Loads the in-tree marshalling module.  (Without it, as in a tree where only the library was built,
+    the same calls go through ctypes.)"""
+    global _fast
+    try:
+        from . import _fastcall
+    except ImportError:
+        return
+    for name in ("gqa_rope_kv_append", "gqa_rope_kv_append_fp8", "gqa_rope_kv_append_int4", "gqa_kv_quantize_int4",
+                 "gqa_kv_dequantize_int4", "gqa_paged_decode_attn_int4", "gqa_paged_multi_query_attn_int4"):
+        _entry[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+    _fast = _fastcall
 
 
 def load_library() -> ctypes.CDLL:
@@ -210,6 +226,7 @@ def load_library() -> ctypes.CDLL:
     lib.gqa_decode_step_int4.argtypes = [vp] * 10 + [i32] * 8 + [f32, i32, i32, vp, sz, vp]
     lib.gqa_decode_step_int4.restype = i32
     _lib = lib
+    _load_fast(lib)
     return lib
 
 
@@ -637,6 +654,24 @@ def _need_rows(t, name, heads, dim, tokens, dev):
     return stride[0] if shape[0] > 1 else shape[1] * dim
 
 
+def _quick(call: str, entry: str, *args) -> bool:
+    """The native marshalling of a call on the current device and stream.  False: not for it (an argument
+    is not what the call takes, or lies on another device); the caller goes on as if it had not asked."""
+    if _fast is None:
+        if _lib is not None:
+            return False
+        load_library()
+        if _fast is None:
+            return False
+    index = _current_device()
+    status = getattr(_fast, call)(_entry[entry], index, _current_stream(index), *args)
+    if status is None:
+        return False
+    if status != GQA_OK:
+        _check(status)
+    return True
+
+
 def _rope(fn, q, k_new, v_new, cos_sin, pools, block_table, positions, seq_ids, interleaved, q_out, stream, dev,
           pool_shape):
     """fn on the pools (and scales) whose addresses `pools` holds."""
@@ -689,6 +724,9 @@ def rope_kv_append(q, k_new, v_new, cos_sin, k_pages, v_pages, block_table, posi
     v_new may be views with a stride between tokens (a fused projection).  Returns the rotated q
     (q_out, which may be q itself when q is contiguous).  Rows with seq_ids[t] < 0 are padding.
     """
+    if stream is None and q_out is not None and _quick("rope", "gqa_rope_kv_append", q, k_new, v_new, cos_sin, q_out,
+                                                       block_table, positions, seq_ids, interleaved, k_pages, v_pages):
+        return q_out
     dev = k_pages.device
     _all(dev, (k_pages, "k_pages", torch.bfloat16), (v_pages, "v_pages", torch.bfloat16))
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
@@ -702,6 +740,9 @@ def rope_kv_append_fp8(q, k_new, v_new, cos_sin, k_pages, v_pages, k_scales, v_s
                        seq_ids: Optional[torch.Tensor] = None, interleaved: bool = False,
                        q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rope_kv_append into e4m3 pools (the fp32 rotated k and v, divided by their scales)."""
+    if stream is None and q_out is not None and _quick("rope", "gqa_rope_kv_append_fp8", q, k_new, v_new, cos_sin, q_out,
+                                                       block_table, positions, seq_ids, interleaved, k_pages, v_pages, k_scales, v_scales):
+        return q_out
     dev = k_pages.device
     _all(dev, (k_pages, "k_pages", torch.uint8), (v_pages, "v_pages", torch.uint8),
          (k_scales, "k_scales", torch.float32), (v_scales, "v_scales", torch.float32))
@@ -727,6 +768,9 @@ def rope_kv_append_int4(q, k_new, v_new, cos_sin, kv_pages, block_table, positio
                         seq_ids: Optional[torch.Tensor] = None, interleaved: bool = False,
                         q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rope_kv_append into a 4-bit pool."""
+    if stream is None and q_out is not None and _quick("rope", "gqa_rope_kv_append_int4", q, k_new, v_new, cos_sin, q_out,
+                                                       block_table, positions, seq_ids, interleaved, kv_pages):
+        return q_out
     dev = kv_pages.device
     shape = _pool_int4(kv_pages, dev)
     return _rope(load_library().gqa_rope_kv_append_int4, q, k_new, v_new, cos_sin, (kv_pages.data_ptr(),), block_table,
@@ -736,6 +780,8 @@ def rope_kv_append_int4(q, k_new, v_new, cos_sin, kv_pages, block_table, positio
 def quantize_pages_int4(k_pages, v_pages, kv_pages: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """A pair of bf16 pools as one 4-bit pool [num_pages, num_kv_heads, page_size / 16, 18 * head_dim]
     (uint8; include/gqa_int4.h gives the format)."""
+    if stream is None and kv_pages is not None and _quick("convert", "gqa_kv_quantize_int4", k_pages, v_pages, kv_pages, 0):
+        return kv_pages
     dev = k_pages.device
     _all(dev, (k_pages, "k_pages", torch.bfloat16), (v_pages, "v_pages", torch.bfloat16))
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
@@ -756,6 +802,9 @@ def quantize_pages_int4(k_pages, v_pages, kv_pages: Optional[torch.Tensor] = Non
 def dequantize_pages_int4(kv_pages, k_pages: Optional[torch.Tensor] = None, v_pages: Optional[torch.Tensor] = None,
                           stream=None):
     """The cached values of a 4-bit pool, rounded to bf16: (k_pages, v_pages)."""
+    if (stream is None and k_pages is not None and v_pages is not None
+            and _quick("convert", "gqa_kv_dequantize_int4", k_pages, v_pages, kv_pages, 1)):
+        return k_pages, v_pages
     dev = kv_pages.device
     P, Hk, ps, D = shape = _pool_int4(kv_pages, dev)
     with _on(dev, stream) as ptr:
@@ -828,6 +877,9 @@ def paged_decode_attn_int4(q, kv_pages, block_table, seq_lens, out: Optional[tor
                            scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
                            stream=None) -> torch.Tensor:
     """paged_decode_attn over a 4-bit pool.  workspace: int4_workspace() (None: the call makes one)."""
+    if (stream is None and out is not None and workspace is not None
+            and _quick("attend", "gqa_paged_decode_attn_int4", q, kv_pages, block_table, seq_lens, out, scale, workspace, 3)):
+        return out
     return _attend_int4(q, kv_pages, block_table, seq_lens, out, scale, workspace, stream, False)
 
 
@@ -835,6 +887,9 @@ def paged_multi_query_attn_int4(q, kv_pages, block_table, seq_lens, out: Optiona
                                 scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
                                 stream=None) -> torch.Tensor:
     """paged_multi_query_attn over a 4-bit pool: q, out [B, Q, H, D]."""
+    if (stream is None and out is not None and workspace is not None
+            and _quick("attend", "gqa_paged_multi_query_attn_int4", q, kv_pages, block_table, seq_lens, out, scale, workspace, 4)):
+        return out
     return _attend_int4(q, kv_pages, block_table, seq_lens, out, scale, workspace, stream, True)
 
 

@@ -1,5 +1,5 @@
 """Build the CUDA library in-tree: csrc/*.cu (+ host-only csrc/*.cpp) -> libgqa_decode.so
-(sm_100a only).
+(sm_100a only), and the binding's marshalling module csrc/fastcall.cc -> _fastcall.so.
 
 Usage:  python -m gqa_decode_attention_04_b200.build [--verbose]
 The shared object is written next to this file so it travels with the source tree.
@@ -10,12 +10,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgqa_decode.so")
+FAST_SOURCE = os.path.join(CSRC, "fastcall.cc")
+FAST = os.path.join(HERE, "_fastcall.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -43,7 +46,29 @@ def needs_rebuild() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_fastcall(verbose: bool = False, force: bool = False) -> str:
+    """The extension module that checks and passes torch tensors (host code only)."""
+    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= os.path.getmtime(FAST_SOURCE):
+        return FAST
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    tmp = FAST + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-shared", "-fPIC", "-std=c++17",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"], FAST_SOURCE, "-o", tmp,
+           "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {FAST_SOURCE}")
+    os.replace(tmp, FAST)
+    return FAST
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
+    build_fastcall(verbose, force)
     if not force and not needs_rebuild():
         return LIB
     objdir = os.path.join(HERE, "_build")

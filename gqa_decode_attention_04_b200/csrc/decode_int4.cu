@@ -57,12 +57,16 @@ struct Cfg {
   static constexpr int kGroups = D / 64;
   static constexpr int kTileBytes = 18 * D;
   static constexpr int kUnitBytes = 2 * kTileBytes;
-  static constexpr int kStages = NT == 1 ? 3 : 5;
+  static constexpr int kStages = 3;
   static constexpr int kCtas = NT == 1 ? 2 : 1;     // per SM
   static constexpr int kRecFloats = kRows * (D + 2);  // a piece: [rows][D], then (reference, sum)
   static constexpr int kRingBytes = kStages * kUnitBytes;
   static_assert(kRingBytes >= kRecFloats * 4, "the last piece of a warp is left in its ring");
-  static constexpr int kSmem = kWarps * kRingBytes;
+  // Where a piece that a range cuts at the front is left: in shared memory if there is room beside the
+  // rings (one CTA per SM), else in the workspace.
+  static constexpr bool kRecHere = NT > 1;
+  static constexpr int kRecBytes = (kRecFloats * 4 + 127) / 128 * 128;
+  static constexpr int kSmem = kWarps * (kRingBytes + (kRecHere ? kRecBytes : 0));
 };
 
 // A piece that a warp's range cut off.
@@ -153,12 +157,11 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   unsigned char* ring = smem + warp * C::kRingBytes;
-  // A warp's pieces: one cut at the front goes to its workspace slot, one cut at the end stays in
-  // its ring, which is idle by then.
-  const int64_t cta_slots = 2 * static_cast<int64_t>(gridDim.x) * C::kRecFloats;
+  // A warp's pieces: one cut at the end stays in its ring, which is idle by then.
   auto record = [&](int i) {
-    return (i & 1) ? reinterpret_cast<float*>(smem + (i / 2) * C::kRingBytes)
-                   : p.slots + cta_slots + (static_cast<int64_t>(blockIdx.x) * kWarps + i / 2) * C::kRecFloats;
+    if (i & 1) return reinterpret_cast<float*>(smem + (i / 2) * C::kRingBytes);
+    if (C::kRecHere) return reinterpret_cast<float*>(smem + kWarps * C::kRingBytes + (i / 2) * C::kRecBytes);
+    return p.slots + (2 * static_cast<int64_t>(gridDim.x) + static_cast<int64_t>(blockIdx.x) * kWarps + i / 2) * C::kRecFloats;
   };
 
   if (lane == 0) {
@@ -888,7 +891,7 @@ namespace {
 template <int D, int NT>
 Int4Plan plan_of() {
   using C = Cfg<D, NT>;
-  return {NT, kWarps, C::kCtas, static_cast<size_t>(C::kSmem), static_cast<size_t>(C::kRecFloats) * (2 + kWarps) * sizeof(float)};
+  return {NT, kWarps, C::kCtas, static_cast<size_t>(C::kSmem), static_cast<size_t>(C::kRecFloats) * (C::kRecHere ? 2 : 2 + kWarps) * sizeof(float)};
 }
 
 template <int D, int NT>
@@ -919,7 +922,10 @@ cudaError_t launch(const Int4DecodeParams& p, int grid, cudaStream_t stream, boo
 
 }  // namespace
 
-// 8 rows per segment while a kv head has no more than that, else 16.
+// 8 rows per segment while a kv head has no more than that, else 16, which widen each tile once for both
+// halves but leave registers for half the warps: a kv head with 16 rows (32 sequences of 512 to 4096
+// tokens, four query tokens) takes 47 us with 16 and 61 with 8; one with 96 (64 of 8192 tokens) 146 and
+// 193 us, and 154 with 24 rows a segment, whose output no longer fits the registers.
 Int4Plan plan_decode_int4(int head_dim, int rows) {
   if (head_dim == 64) return rows <= 8 ? plan_of<64, 1>() : plan_of<64, 2>();
   return rows <= 8 ? plan_of<128, 1>() : plan_of<128, 2>();

@@ -418,3 +418,47 @@ def test_two_graphs_replayed_at_once(cuda_device):
     torch.cuda.synchronize()
     gq.check_device_error()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_given_outputs_go_the_native_way_and_give_the_same(cuda_device):
+    """Calls whose outputs are given are marshalled natively: the same results, the same refusals."""
+    assert gq._fast is not None
+    rng = np.random.default_rng(41)
+    lens = [60, 33]
+    bt, pages = make_table(rng, lens, 16)
+    k, v = (bf16(rng.standard_normal((pages, 2, 16, 64))).to(cuda_device) for _ in range(2))
+    dbt, dsl = device(cuda_device, bt, np.array(lens, np.int32))
+    pool = gq.quantize_pages_int4(k, v)
+    given = torch.empty_like(pool)
+    assert gq.quantize_pages_int4(k, v, given) is given and torch.equal(given, pool)
+    a, b = torch.empty_like(k), torch.empty_like(k)
+    gq.dequantize_pages_int4(pool, a, b)
+    assert all(torch.equal(x, y) for x, y in zip((a, b), gq.dequantize_pages_int4(pool)))
+    ws = gq.int4_workspace()
+    for shape, fn in (((2, 8, 64), gq.paged_decode_attn_int4), ((2, 3, 8, 64), gq.paged_multi_query_attn_int4)):
+        q = bf16(rng.standard_normal(shape)).to(cuda_device)
+        out = torch.empty_like(q)
+        for scale in (None, 0.3):
+            assert fn(q, pool, dbt, dsl, out, scale, ws) is out
+            assert torch.equal(out, fn(q, pool, dbt, dsl, scale=scale))
+        for bad in (dict(out=out.float()), dict(out=out[..., :32]), dict(workspace=ws[:100].clone()), dict(scale=float("nan")),
+                    dict(workspace=ws.float()), dict(out=out.cpu()), dict(scale="x")):
+            with pytest.raises((ValueError, TypeError, gq.GQAError)):
+                fn(q, pool, dbt, dsl, **{**dict(out=out, scale=0.3, workspace=ws), **bad})
+        for bad in (dict(kv_pages=pool[..., :-1]), dict(block_table=dbt[:1]), dict(seq_lens=dsl.long()), dict(q=q[0])):
+            with pytest.raises((ValueError, TypeError, gq.GQAError)):
+                fn(**{**dict(q=q, kv_pages=pool, block_table=dbt, seq_lens=dsl, out=out, workspace=ws), **bad})
+    with pytest.raises(ValueError):
+        gq.quantize_pages_int4(k, v, given[:1])
+    with pytest.raises((ValueError, TypeError)):
+        gq.dequantize_pages_int4(pool, a, b.float())
+    x = torch.zeros(2, 12, 64, dtype=torch.bfloat16, device=cuda_device)
+    qkv = dict(q=x[:, :8], k_new=x[:, 8:10], v_new=x[:, 10:], cos_sin=torch.ones(100, 64, device=cuda_device),
+               kv_pages=pool, block_table=dbt, positions=dsl - 1, q_out=torch.empty(2, 8, 64, dtype=torch.bfloat16, device=cuda_device))
+    assert gq.rope_kv_append_int4(**qkv) is qkv["q_out"]
+    for bad in (dict(q=x[:, :8, ::2]), dict(k_new=x[:, 8:11]), dict(q_out=x[:, :8]), dict(positions=dsl.long()), dict(cos_sin=torch.ones(100, 80, device=cuda_device)),
+                dict(seq_ids=dsl[:1]), dict(block_table=dbt[:1]), dict(q=x.transpose(0, 1))):
+        with pytest.raises((ValueError, TypeError, gq.GQAError)):
+            gq.rope_kv_append_int4(**{**qkv, **bad})
+    torch.cuda.synchronize()
+    gq.check_device_error()
