@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   __shared__ __align__(8) uint64_t full[kWarps][C::kStages];
   __shared__ Piece pieces[2 * kWarps];
   __shared__ int2 last_of[2];
+  __shared__ Split kept;  // for the merges: the loop has no registers for it
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
@@ -197,10 +198,13 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     int64_t total = 0;
     for (int w = 0; w < kWarps; ++w) total += scan[w];
     split.total = total * segs;
-    // as many warps as there are units, if that is fewer
-    split.workers = min(static_cast<int64_t>(gridDim.x) * kWarps, split.total);
+    // A batch of a few units is not cut finer than a segment of one: two sequences of 17 and 40 tokens
+    // take 6.1 us whole and 7.9 cut, merges being most of it.
+    const int64_t least = split.total <= 4 * kWarps ? kSegCost + 1 : 1;
+    split.workers = min(static_cast<int64_t>(gridDim.x) * kWarps, quotient(split.total + least - 1, least));
     split.per = split.total == 0 ? 0 : quotient(split.total, split.workers);
     split.rem = split.total - split.per * split.workers;
+    if (threadIdx.x == 0) kept = split;
   }
   const int64_t me = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   int64_t pos = split.start(me);
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     int pb = b, phead = seg / p.n_rt, prt = seg - phead * p.n_rt, plen = len, pleft = left;
     int punits = units_of(len) - unit0;  // units of the segment not issued yet
     int win = 2 * unit0, in_win = 16;    // the window's first tile; its next unit (16: past it)
-    int pstage = 0, ahead = -1;          // ahead: this lane's page of the next window
+    int ahead = -1;                      // this lane's page of the next window
     uint32_t bad = 0;                    // two bits per stage: no data behind the tile
     uint64_t addr = 0;
     const uint32_t ring_at = ptx::smem_u32(ring) + (lane & 1) * C::kTileBytes, bar_at = ptx::smem_u32(&full[warp][0]);
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
       const int block = p.tpp_magic != 0 ? fast_div(tile, p.tpp_magic, p.tpp_shift) : tile;
       return tile * int4::kTile < plen ? __ldg(p.block_table + static_cast<int64_t>(pb) * p.max_blocks + block) : -1;
     };
-    auto produce = [&]() {
+    auto produce = [&](int pstage) {  // into the stage that is free
       if (pleft <= 0) return;
       if (in_win == 16) {  // the next 32 tiles
         const int tile = win + lane;
@@ -291,7 +295,6 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           ptx::mbar_arrive(bar);
         }
       }
-      pstage = pstage + 1 == C::kStages ? 0 : pstage + 1;
       ++in_win;
       --pleft;
       if (--punits == 0) {  // the next segment
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     };
     ahead = page_of(win + lane);
     __syncwarp();
-    for (int s = 0; s < C::kStages; ++s) produce();
+    for (int s = 0; s < C::kStages; ++s) produce(s);
 
     // this lane's places in a tile
     const uint32_t at_k = g * (D / 2) + t * (D / 8), at_par = L4::kParams + g * (8 * G);
@@ -616,9 +619,9 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           dead = true;
           if (lane == 0) atomicOr(p.err, kErrTimeout);
           if (!p.arm_without_copy) {  // nothing may still be landing when the ring is written or given up
-            int in_flight = pstage - stage;
-            if (in_flight <= 0) in_flight += C::kStages;
-            for (; in_flight > 0; --in_flight) {
+            // (a stage that nothing was sent to is waited for in vain)
+#pragma unroll 1
+            for (int k = 0; k < C::kStages; ++k) {
               ptx::mbar_wait_bounded(bar_at + 8 * stage, parity, p.wait_limit_ns);
               if (++stage == C::kStages) stage = 0, parity ^= 1;
             }
@@ -637,9 +640,9 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           for (int k = 0; k < 2; ++k)
             if ((lost >> k & 1u) == 0) attend(at + k * C::kTileBytes, tok0 + k * int4::kTile, std::true_type{});
         }
-        if (++stage == C::kStages) stage = 0, parity ^= 1;
         __syncwarp();  // every lane has read the stage
-        produce();
+        produce(stage);
+        if (++stage == C::kStages) stage = 0, parity ^= 1;
       }
 
       // ---- end of the piece
@@ -723,8 +726,8 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   __syncthreads();
 
   // ---- merge what the ranges cut: over the CTA's warps, then over CTAs
-  const int64_t cta_start = split.start(static_cast<int64_t>(blockIdx.x) * kWarps);
-  const int64_t cta_end = split.start(static_cast<int64_t>(blockIdx.x + 1) * kWarps);
+  const int64_t cta_start = kept.start(static_cast<int64_t>(blockIdx.x) * kWarps);
+  const int64_t cta_end = kept.start(static_cast<int64_t>(blockIdx.x + 1) * kWarps);
   auto out_row = [&](int b, int seg, int r) -> uint16_t* {
     const int head = seg / p.n_rt, row = (seg - head * p.n_rt) * C::kRows + r;
     if (row >= p.rows) return nullptr;
@@ -732,6 +735,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     return p.out + ((static_cast<int64_t>(b) * p.q_len + tok) * p.num_heads + static_cast<int64_t>(head) * p.group +
                     (row - tok * p.group)) * D;
   };
+  static_assert(kWarps * C::kRecFloats * 4 <= C::kSmem, "a part per warp beside one another");
   static_assert(C::kRows <= 4 * kWarps, "a warp has four rows of a segment at most");
   constexpr int kMl = C::kRows * D;  // (reference, sum) of the rows, behind the rows
   const int col = 4 * (lane % (D / 4));
@@ -821,8 +825,8 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
         if (into == nullptr) {
           if (lane < D / 4) st_bf16x4(out_row(b, seg, r0 + k) + col, acc[k], l != 0.0f ? 1.0f / l : 0.0f);
         } else {
-          if (lane < D / 4) __stcg(reinterpret_cast<float4*>(into + (r0 + k) * D + col), acc[k]);
-          if (lane == 0) __stcg(reinterpret_cast<float2*>(into + kMl + 2 * (r0 + k)), make_float2(t, l));
+          if (lane < D / 4) *reinterpret_cast<float4*>(into + (r0 + k) * D + col) = acc[k];
+          if (lane == 0) *reinterpret_cast<float2*>(into + kMl + 2 * (r0 + k)) = make_float2(t, l);
         }
       }
     }
@@ -863,8 +867,8 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     const int i = outward[threadIdx.x];
     if (i >= 0) {
       const Piece pc = pieces[i];
-      const int from = static_cast<int>(split.owner(pc.start) / kWarps);
-      const int to = static_cast<int>(split.owner(pc.start + pc.units - 1) / kWarps);
+      const int from = static_cast<int>(kept.owner(pc.start) / kWarps);
+      const int to = static_cast<int>(kept.owner(pc.start + pc.units - 1) / kWarps);
       if (atomicAdd(p.counters + from, 1) == to - from) ctas = make_int2(from, to);
     }
     last_of[threadIdx.x] = ctas;
@@ -879,10 +883,10 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     if (threadIdx.x == 0) p.counters[from] = 0;
     // the first CTA's part is its second slot, the others' their first
     auto part = [&](int c) { return p.slots + (2 * static_cast<int64_t>(from + c) + (c == 0)) * C::kRecFloats; };
-    if (4 * warp < rows_of(pc.seg))
-      merge(pc.b, pc.seg, 4 * warp, rows_of(pc.seg), to - from + 1, 0xffffu, part,
-            [](const float* x) { return __ldcg(reinterpret_cast<const float2*>(x)); },
-            [](const float* x) { return __ldcg(reinterpret_cast<const float4*>(x)); }, nullptr);
+    auto far2 = [](const float* x) { return __ldcg(reinterpret_cast<const float2*>(x)); };
+    auto far4 = [](const float* x) { return __ldcg(reinterpret_cast<const float4*>(x)); };
+    const int count = to - from + 1, valid = rows_of(pc.seg), quads = (valid + 3) / 4;
+    if (warp < quads) merge(pc.b, pc.seg, 4 * warp, valid, count, 0xffffu, part, far2, far4, nullptr);
   }
 }
 
