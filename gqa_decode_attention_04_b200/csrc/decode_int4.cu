@@ -198,9 +198,13 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     int64_t total = 0;
     for (int w = 0; w < kWarps; ++w) total += scan[w];
     split.total = total * segs;
-    // A batch of a few units is not cut finer than a segment of one: two sequences of 17 and 40 tokens
-    // take 6.1 us whole and 7.9 cut, merges being most of it.
-    const int64_t least = split.total <= 4 * kWarps ? kSegCost + 1 : 1;
+    // Least work of a warp.  Few long segments are not cut into more than is merged in the time that it
+    // saves: a unit takes 0.8 us, a warp merges four CTAs' parts of a segment in 1 us, and n units a
+    // segment in ranges of x make n / 8 x parts: x = sqrt(n / 26).  (One sequence of 131072 tokens and one
+    // kv head: 31 us, and 63 cut as finely as there are warps; three of 30000 24 and 32.)  A batch of a few units is not cut finer
+    // than a segment of one: two sequences of 17 and 40 tokens take 6.2 us whole and 7.9 cut.
+    int64_t least = static_cast<int64_t>(sqrtf(__fdividef(static_cast<float>(split.total), 26.0f * segs * p.num_seqs)));
+    least = max(least, split.total <= 4 * kWarps ? int64_t{kSegCost + 1} : int64_t{1});
     split.workers = min(static_cast<int64_t>(gridDim.x) * kWarps, quotient(split.total + least - 1, least));
     split.per = split.total == 0 ? 0 : quotient(split.total, split.workers);
     split.rem = split.total - split.per * split.workers;
