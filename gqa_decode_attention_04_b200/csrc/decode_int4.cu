@@ -84,7 +84,13 @@ constexpr int kUnit = 2 * int4::kTile;  // tokens per step of a warp
 // 37.9, 36.6, 36.0, 36.1, and with four query tokens 61, 51.9, 50.6, 48.7.
 constexpr int kSegCost = 3;
 
-__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int units_of(int len) {
+  return static_cast<int>((static_cast<unsigned>(len) + (kUnit - 1)) / kUnit);  // (len may be near 2^31)
+}
+// Whether a sequence of len tokens has a tile of this number.
+__device__ __forceinline__ bool has_tile(int tile, int len) {
+  return static_cast<unsigned>(tile) * int4::kTile < static_cast<unsigned>(len);
+}
 __device__ __forceinline__ int cost_of(int len) { return len > 0 ? units_of(len) + kSegCost : 0; }
 
 // The length of sequence b, 0 if it is out of range.
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     const uint32_t ring_at = ptx::smem_u32(ring) + (lane & 1) * C::kTileBytes, bar_at = ptx::smem_u32(&full[warp][0]);
     auto page_of = [&](int tile) {
       const int block = p.tpp_magic != 0 ? fast_div(tile, p.tpp_magic, p.tpp_shift) : tile;
-      return tile * int4::kTile < plen ? __ldg(p.block_table + static_cast<int64_t>(pb) * p.max_blocks + block) : -1;
+      return has_tile(tile, plen) ? __ldg(p.block_table + static_cast<int64_t>(pb) * p.max_blocks + block) : -1;
     };
     auto produce = [&](int pstage) {  // into the stage that is free
       if (pleft <= 0) return;
@@ -276,7 +282,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
         const int tile = win + lane;
         const int block = p.tpp_magic != 0 ? fast_div(tile, p.tpp_magic, p.tpp_shift) : tile;
         const int page = ahead;
-        const bool wanted = tile * int4::kTile < plen;
+        const bool wanted = has_tile(tile, plen);
         const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
         const uint32_t at = (static_cast<uint32_t>(page) * p.num_kv_heads + phead) * p.tiles_per_page +
                             (tile - block * p.tiles_per_page);

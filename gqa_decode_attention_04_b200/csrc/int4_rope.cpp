@@ -150,6 +150,7 @@ gqa_status decode(const void* q, const void* kv_pages, const int32_t* block_tabl
   if (num_seqs > 65536) return set_error(GQA_ERR_UNSUPPORTED, "num_seqs > 65536");
   if (q_len < 1) return set_error(GQA_ERR_INVALID_ARG, "q_len %d < 1", q_len);
   if (num_heads < 1) return set_error(GQA_ERR_INVALID_ARG, "sizes must be positive");
+  if (num_heads > INT32_MAX / 4096) return set_error(GQA_ERR_UNSUPPORTED, "too many heads");
   gqa_status s = check_pool(num_kv_heads, head_dim, page_size);
   if (s != GQA_OK) return s;
   if (num_heads % num_kv_heads != 0)

@@ -448,18 +448,6 @@ __device__ __forceinline__ uint32_t e4m3x2_hi(uint32_t w) {
   return r;
 }
 
-// Loads, from shared or global memory, that see what other CTAs wrote before a fence.
-__device__ __forceinline__ float4 ld_relaxed_f4(const float* p) {
-  float4 v;
-  asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ float2 ld_relaxed_f2(const float* p) {
-  float2 v;
-  asm volatile("ld.relaxed.gpu.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
-  return v;
-}
-
 __device__ __forceinline__ float4 ld_cg_f4(const float* p) {
   return __ldcg(reinterpret_cast<const float4*>(p));
 }

@@ -462,3 +462,53 @@ def test_given_outputs_go_the_native_way_and_give_the_same(cuda_device):
             gq.rope_kv_append_int4(**{**qkv, **bad})
     torch.cuda.synchronize()
     gq.check_device_error()
+
+
+def test_the_longest_sequence(cuda_device):
+    """2^31 - 256 tokens, all in one page: equal weights on each copy of it, so the output is that of one.
+
+    The sums take the same tokens again and again, rounded at each step.  A warp has n tokens: the work of
+    8 query rows is cut evenly over 16 warps per SM.  Its weights' sums go to eight lanes
+    a row (n / 8 steps of 2^-24 relative), its outputs' step by step over 16 tokens (n / 16 of 2^-23): n
+    2^-26 of the largest output, which is of one sign here, for the weights' sum, the minima's and the
+    outputs', and what the attention over one page may be off beside that.
+    """
+    rng = np.random.default_rng(51)
+    ps, d, h = 256, 64, 8
+    blocks = (2 ** 31 - 1) // ps
+    k = (rng.standard_normal((1, 1, ps, d))).astype(np.float32)
+    v = (2 + 0.25 * rng.standard_normal((1, 1, ps, d))).astype(np.float32)
+    pool = oracle.int4_pool_from_rows(k, v)
+    q = bf16(rng.standard_normal((1, h, d)))
+    one = np.zeros((1, 1), np.int32)
+    q4 = q.float().double().numpy()[:, None]
+    want = oracle.paged_multi_query_attention_int4(q4, pool, one, [ps], d ** -0.5)
+    bound = attention_bound(q4, pool, one, [ps], d ** -0.5)
+    lens = torch.tensor([blocks * ps], dtype=torch.int32, device=cuda_device)
+    table = torch.zeros((1, blocks), dtype=torch.int32, device=cuda_device)
+    out = gq.paged_decode_attn_int4(q.to(cuda_device), torch.from_numpy(pool).to(cuda_device), table, lens)
+    gq.check_device_error()
+    n = blocks * ps / 16 / torch.cuda.get_device_properties(cuda_device).multi_processor_count
+    assert np.all(np.abs(gpu_f64(out).reshape(want.shape) - want) <= bound + 3 * n * 2.0 ** -26 * np.abs(want).max())
+
+
+def test_tensors_without_plain_memory_are_refused(cuda_device):
+    """Nested and sparse tensors throw when they are asked for sizes or strides: an exception, no more."""
+    pool = torch.zeros(2, 1, 1, 18 * 64, dtype=torch.uint8, device=cuda_device)
+    x = torch.zeros(2, 8, 64, dtype=torch.bfloat16, device=cuda_device)
+    table = torch.zeros(2, 1, dtype=torch.int32, device=cuda_device)
+    lens = torch.ones(2, dtype=torch.int32, device=cuda_device)
+    ws = gq.int4_workspace()
+    for odd in (torch.nested.nested_tensor([x[0], x[1, :3]]), x.to_sparse()):
+        for kw in (dict(q=odd), dict(out=odd)):
+            with pytest.raises(Exception):
+                gq.paged_decode_attn_int4(**{**dict(q=x, kv_pages=pool, block_table=table, seq_lens=lens,
+                                                    out=torch.empty_like(x), workspace=ws), **kw})
+        with pytest.raises(Exception):
+            gq.rope_kv_append_int4(odd, x[:, :1], x[:, :1], torch.ones(4, 64, device=cuda_device), pool, table, lens,
+                                   q_out=torch.empty_like(x))
+        pages = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16, device=cuda_device)
+        with pytest.raises(Exception):
+            gq.quantize_pages_int4(pages.to_sparse(), pages, pool)
+    torch.cuda.synchronize()
+    gq.check_device_error()

@@ -127,6 +127,7 @@ def _decode(lib, B=2, Q=None, H=4, Hk=1, D=64, ps=16, scale=0.125, MB=4, pages=8
     (dict(ws=0), -1), (dict(ws=OK + 128), -1), (dict(ws_bytes=(16 << 20) - 1), -1),
     (dict(Q=0), -1), (dict(Q=33), -2), (dict(Q=3, H=96, Hk=2), -2),
     (dict(B=0), 0), (dict(B=0, Q=32), 0), (dict(B=0, ptr=0, ws=0), 0),
+    (dict(B=0, H=1 << 20, Hk=1 << 20), -2),
 ])
 def test_decode_refusals(lib, kw, status):
     assert _decode(lib, **kw) == status
