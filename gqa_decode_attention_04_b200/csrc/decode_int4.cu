@@ -13,22 +13,32 @@
 //   q is scaled by a power of two per row so that its largest element lies in [2^14, 2^15):
 // exact in fp16 for elements within 2^-28 of it (bf16 has 8 significant bits), and the products
 // with c * 2^-24 stay normal in fp32.
-//   p s is rounded to fp16.  Steps may be of any size, so each row carries a power of two F per
-// group that keeps p s F below 2^15; it moves with the running maximum.  Scores, sums and
-// outputs are fp32.
+//   The minima's part of a score is one more MMA of depth 4 per tile, in tf32: m is exact there, and
+// sum(q_g) goes in as two parts of 11 bits.
+//   p s is rounded to fp16.  Steps may be of any size, so each row carries a power of two F that
+// keeps p s F below 2^15; it moves with the running maximum, which itself moves only when a score
+// passes it by 2^12.  Scores, sums and outputs are fp32.
 //
-// Bound: HBM at small groups -- 9/8 D bytes per token and kv head.  At that rate a tile of 16
-// tokens has to be done every ~100 cycles per SM, which leaves about 400 issue slots a tile,
-// and that is what the shape is for: warps that never wait for one another.
+// Bound: HBM at small groups on paper -- 9/8 D bytes per token and kv head -- but in fact the
+// instructions that turn codes into MMA operands, whatever the number of query rows: about 320 per
+// tile of 16 tokens and row tile, two thirds of them on the integer pipe at half rate.  4 sequences of
+// 131072 tokens, 8 kv heads, 8 rows each: 136 us (4.4 TB/s, 68 % of a copy's rate), 133 with the pool in L2,
+// 107 with the copies alone.  256 sequences of 1 to 32768 tokens: 183 us (5.1 TB/s, 78 %).  More rows
+// widen each tile again for every 16: 96 rows (64 sequences of 8192 tokens, one kv head) 145 us, 0.18
+// PFLOP/s.
 //
-// Work.  The list of tiles (sequence, kv head, row tile, 16-token tile), in that order, is cut
-// into one equal contiguous range per WARP.  Each warp streams its range through its own ring
-// of kStages tiles in shared memory (one bulk copy per tile: K, V and parameters lie together),
-// and keeps the running maximum, sum and output of its current segment in registers; there is no
-// producer warp and no barrier in the loop.  A segment wholly inside a warp's range is written out
-// at once.  What a range cuts is left in shared memory (at most the first and the last segment of
-// a warp), merged over the CTA's warps after one __syncthreads, and over CTAs through two
-// workspace slots per CTA: the last CTA to arrive at a segment's counter merges it.
+// Work.  The list of units (sequence, kv head, row tile, 32 tokens), in that order, is cut into one
+// contiguous range of equal cost per WARP.  Each warp streams its range through its own ring of
+// kStages units in shared memory (one bulk copy per tile of 16 tokens: K, V and parameters lie
+// together), and keeps the running maximum, sum and output of its current segment in registers;
+// there is no producer warp and no barrier in the loop.  The copies' cursor runs kStages units ahead;
+// lane i holds the address of the i-th tile of a window of 32, so a unit costs no index arithmetic.
+// (One producer warp for the CTA instead, with registers moved to the others: 142 us for 135, and
+// 42 for 36 on 32 sequences of 512 to 4096 tokens.)  A segment wholly inside a warp's range is written
+// out at once.  What a range cuts is left in shared memory or the workspace (at most the first and the
+// last segment of a warp), merged over the CTA's warps after one __syncthreads, and over CTAs through
+// two workspace slots per CTA: the last CTA to arrive at a segment's counter merges it.  Which order
+// the CTAs arrive in changes nothing: the parts are summed in the order of the list.
 //
 // The S tile is computed transposed, S^T = K Q^T (tokens on the MMA's 16-row side, 8 query
 // rows on the other), so a group of 4 or 8 heads needs no padding to 16.
@@ -154,7 +164,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
 
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t excl[32 * kWarps];  // tiles of the sequences before each thread's chunk
+  __shared__ int64_t excl[32 * kWarps];  // cost of the sequences before each thread's chunk
   __shared__ int64_t scan[kWarps];
   __shared__ __align__(8) uint64_t full[kWarps][C::kStages];
   __shared__ Piece pieces[2 * kWarps];
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     pieces[2 * warp + 1].units = 0;
   }
 
-  // ---- the split: tiles before each thread's chunk of sequences
+  // ---- the split: cost before each thread's chunk of sequences
   const int segs = p.num_kv_heads * p.n_rt;  // segments per sequence
   const int chunk = (p.num_seqs + 32 * kWarps - 1) / (32 * kWarps);
   {
@@ -207,8 +217,9 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     // Least work of a warp.  Few long segments are not cut into more than is merged in the time that it
     // saves: a unit takes 0.8 us, a warp merges four CTAs' parts of a segment in 1 us, and n units a
     // segment in ranges of x make n / 8 x parts: x = sqrt(n / 26).  (One sequence of 131072 tokens and one
-    // kv head: 31 us, and 63 cut as finely as there are warps; three of 30000 24 and 32.)  A batch of a few units is not cut finer
-    // than a segment of one: two sequences of 17 and 40 tokens take 6.2 us whole and 7.9 cut.
+    // kv head: 31 us, and 63 cut as finely as there are warps; three of 30000 24 and 32.)  A batch of a few
+    // units is not cut finer than a segment of one: two sequences of 17 and 40 tokens take 6.2 us whole
+    // and 7.9 cut.
     int64_t least = static_cast<int64_t>(sqrtf(__fdividef(static_cast<float>(split.total), 26.0f * segs * p.num_seqs)));
     least = max(least, split.total <= 4 * kWarps ? int64_t{kSegCost + 1} : int64_t{1});
     split.workers = min(static_cast<int64_t>(gridDim.x) * kWarps, quotient(split.total + least - 1, least));
@@ -223,7 +234,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   ptx::pdl_wait_prerequisites();  // q and the pool may be written by the preceding append
 
   if (pos < end) {
-    // ---- find the first tile: the chunk, then the sequence in it
+    // ---- find the first unit: the chunk, then the sequence in it
     const int64_t unit = quotient(pos, segs);  // in units of a sequence's one segment
     int ci = 0;
     for (int i = 0; i < kWarps; ++i) {

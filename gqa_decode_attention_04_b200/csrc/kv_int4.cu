@@ -4,7 +4,9 @@
 // thread (tau, j) of a tile holds channels 16 j .. 16 j + 15 of token tau, first of K, then of V
 // (16 channels a thread, not 8: the minimum, the step and its reciprocal are found half as often).
 // A block does 256 threads' worth of tiles.
-// Bound: HBM (4 D bytes of bf16 and 9/8 D bytes of the 4-bit cache per token and kv head).
+// Bound: HBM (4 D bytes of bf16 and 9/8 D bytes of the 4-bit cache per token and kv head).  9001 pages
+// of 16 tokens and 8 kv heads, there and back: 273 us for 1.51 GB, 5.5 TB/s, 85 % of a copy's rate (349 us with 8
+// channels a thread and plain divisions).
 #include "int4_codec.cuh"
 #include "internal.cuh"
 #include "ptx.cuh"

@@ -7,6 +7,11 @@
 // of a channel lies rotary_dim / 16 lanes away: the pair is brought together by shuffles of
 // the packed bf16 words, so no element is read twice.  A thread keeps its cos and sin for all
 // the rows it handles (the same channels of several heads of one token).
+//   Measured: one token of 32 + 8 heads 2.1 us and 256 of them into bf16 3.5 us (the launch, then two
+// dependent loads: position, then block table and angles); 5987 tokens of 12 + 2 heads of 64 into e4m3 6.5
+// us (3.7 TB/s), 16384 of 32 + 8 of 128 into bf16 81 us (5.1 TB/s, 77 % of a copy's rate), of 64 + 8 into 4
+// bits 137 us (4.6 TB/s), where the instructions of the rotation and the quantiser are what is left between
+// it and HBM.
 #include <climits>
 
 #include <cuda_fp8.h>
@@ -20,10 +25,10 @@ namespace gqa {
 namespace {
 
 constexpr int kThreads = 256;
-// Rows of a thread whose loads are in flight together, and blocks per SM that the registers are
-// held down for: 16384 tokens of 64 + 16 heads into 4 bits with the pool read back take 182 us with
-// (4, 4), 206 with (4, 3), 191 with (4, 5), 201 with (3, 4); 5987 tokens of 12 + 4 heads into e4m3
-// 6.3, 6.0, 8.4, 6.6 us.
+// q rows of a thread whose loads are in flight together, and blocks per SM that the registers are held
+// down for: 16384 tokens of 64 + 8 heads into 4 bits with the pool read back take 169 us with (4, 4), 178
+// with (4, 5), 187 with (4, 3), 192 with (3, 4), 167 with (2, 4); of 32 + 8 heads into e4m3 87 us with (4, 4), 98 with
+// (4, 3), 90 with (4, 5); into bf16 81 with (4, 4), 93 with (2, 4).
 constexpr int kBatch = 4, kBlocks = 4;
 
 __device__ __forceinline__ uint32_t codes2(float a, float b, float s) {
@@ -55,23 +60,43 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
     row = (blockIdx.x - t * p.chunks) * kSlots + slot;
     stride = INT_MAX / 2;
   }
+  // The first rows are on their way before it is known where they go, or that they are padding: what a
+  // block waits for is latency.  (256 tokens into bf16 4.6 us with
+  // the rows loaded after the page is known, 3.9 so; 16384 of 64 + 8 heads into 4 bits, read back, 182 and 169.)
+  const bool here = t < p.num_tokens;
+  constexpr int kQ = MANY ? kBatch : 1;
+  const int cached = 2 * p.num_kv_heads;
+  const uint4* q_in = reinterpret_cast<const uint4*>(p.q + t * p.q_stride) + j;
+  auto load_q = [&](int r0, uint4 (&in)[kQ]) {
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) {
+      in[k] = make_uint4(0, 0, 0, 0);
+      if (here && r0 + k * stride < p.num_heads) in[k] = q_in[(r0 + k * stride) * kLanes];
+    }
+  };
+  auto load_cached = [&](int r) {
+    uint4 in = make_uint4(0, 0, 0, 0);
+    if (here && r >= 0 && r < cached) {
+      const uint16_t* src = r < p.num_kv_heads ? p.k + t * p.k_stride + r * D : p.v + t * p.v_stride + (r - p.num_kv_heads) * D;
+      in = *(reinterpret_cast<const uint4*>(src) + j);
+    }
+    return in;
+  };
+  const int first_cached = MANY ? row : row - p.num_heads;
+  uint4 q_rows[kQ];
+  load_q(row, q_rows);
+  uint4 c_row = load_cached(first_cached);
   // (a warp may hold rows of several tokens, of which some are skipped: all its lanes stay for the shuffles)
-  bool live = t < p.num_tokens;
+  bool live = here;
   const int s = !live ? -1 : (p.seq_ids != nullptr ? __ldg(p.seq_ids + t) : t);
   const int pos = live ? __ldg(p.positions + t) : 0;
   live = s >= 0;  // else padding
   int page = -1, in_page = 0;
-  if (live) {
-    if (s < p.num_seqs && pos >= 0 && pos < p.max_positions &&
-        static_cast<int64_t>(pos) < static_cast<int64_t>(p.max_blocks) * p.page_size) {
-      const int block = p.page_size == 1 ? pos : fast_div(pos, p.ps_magic, p.ps_shift);
-      in_page = pos - block * p.page_size;
-      page = __ldg(p.block_table + static_cast<int64_t>(s) * p.max_blocks + block);
-    }
-    if (page < 0 || page >= p.num_pages) {
-      live = false;
-      if (row == 0 && j == 0) atomicOr(p.err, kErrBounds);
-    }
+  if (live && s < p.num_seqs && pos >= 0 && pos < p.max_positions &&
+      static_cast<int64_t>(pos) < static_cast<int64_t>(p.max_blocks) * p.page_size) {
+    const int block = p.page_size == 1 ? pos : fast_div(pos, p.ps_magic, p.ps_shift);
+    in_page = pos - block * p.page_size;
+    page = __ldg(p.block_table + static_cast<int64_t>(s) * p.max_blocks + block);
   }
 
   const int half_lanes = p.rotary_dim / 16;  // lanes of the first half of the rotated channels
@@ -81,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
   float c[8], sn[8];
 #pragma unroll
   for (int m = 0; m < 8; ++m) c[m] = 1.0f, sn[m] = 0.0f;
-  if (rotated && live) {
+  if (rotated && live && static_cast<unsigned>(pos) < static_cast<unsigned>(p.max_positions)) {
     const float* at = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim;
     if (p.interleaved) {  // pairs (2 m, 2 m + 1), m = 4 j .. 4 j + 3
       const float4 a = __ldg(reinterpret_cast<const float4*>(at) + j);
@@ -99,6 +124,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
         sn[4 * h] = sign * b.x; sn[4 * h + 1] = sign * b.y; sn[4 * h + 2] = sign * b.z; sn[4 * h + 3] = sign * b.w;
       }
     }
+  }
+  if (live && (page < 0 || page >= p.num_pages)) {
+    live = false;
+    if (row == 0 && j == 0) atomicOr(p.err, kErrBounds);
   }
   // the lane that holds the other half of this lane's pairs (itself where nothing is exchanged)
   const int lane = threadIdx.x & 31;
@@ -132,54 +161,34 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
   };
 
   // ---- q
-  const uint4* q_in = reinterpret_cast<const uint4*>(p.q + t * p.q_stride) + j;
   uint4* q_out = reinterpret_cast<uint4*>(p.q_out + static_cast<int64_t>(t) * p.num_heads * D) + j;
-  constexpr int kQ = MANY ? kBatch : 1;
 #pragma unroll 1
-  for (int r0 = row; __any_sync(0xffffffffu, r0 < p.num_heads); r0 += kQ * stride) {
-    uint4 in[kQ];
-#pragma unroll
-    for (int k = 0; k < kQ; ++k) {
-      in[k] = make_uint4(0, 0, 0, 0);
-      if (live && r0 + k * stride < p.num_heads) in[k] = q_in[(r0 + k * stride) * kLanes];
-    }
+  for (int r0 = row; __any_sync(0xffffffffu, r0 < p.num_heads);) {
 #pragma unroll
     for (int k = 0; k < kQ; ++k) {
       float x[8];
-      rotate(in[k], x);
+      rotate(q_rows[k], x);
       if (live && r0 + k * stride < p.num_heads) q_out[(r0 + k * stride) * kLanes] = int4::pack8(x);
     }
     if (!MANY) break;
+    r0 += kQ * stride;
+    load_q(r0, q_rows);
   }
 
   // ---- k, then v
-  const int cached = 2 * p.num_kv_heads;
-  constexpr int kC = MANY ? 2 : 1;
 #pragma unroll 1
-  for (int r0 = MANY ? row : row - p.num_heads; __any_sync(0xffffffffu, r0 >= 0 && r0 < cached); r0 += kC * stride) {
-    uint4 in[kC];
-#pragma unroll
-    for (int k = 0; k < kC; ++k) {
-      const int r = r0 + k * stride;
-      in[k] = make_uint4(0, 0, 0, 0);
-      if (live && r >= 0 && r < cached) {
-        const uint16_t* src = r < p.num_kv_heads ? p.k + t * p.k_stride + r * D : p.v + t * p.v_stride + (r - p.num_kv_heads) * D;
-        in[k] = *(reinterpret_cast<const uint4*>(src) + j);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kC; ++k) {
-      const int r = r0 + k * stride;
-      if (kC > 1 && !__any_sync(0xffffffffu, r < cached)) break;
-      const bool is_v = r >= p.num_kv_heads;
-      float x[8], turned[8];
-      int4::unpack8(in[k], x);
-      rotate(in[k], turned);
+  for (int r = first_cached; __any_sync(0xffffffffu, r >= 0 && r < cached);) {
+    const bool is_v = r >= p.num_kv_heads;
+    float x[8], turned[8];
+    int4::unpack8(c_row, x);
+    if (__any_sync(0xffffffffu, !is_v)) {
+      rotate(c_row, turned);
 #pragma unroll
       for (int m = 0; m < 8; ++m) x[m] = is_v ? x[m] : turned[m];
-      uint32_t pair = 0, word[1] = {0};
-      if (CACHE == kCacheInt4) int4::quantize<1>(x, word, pair);  // (by the whole warp: it shuffles)
-      if (!live || r < 0 || r >= cached) continue;
+    }
+    uint32_t pair = 0, word[1] = {0};
+    if (CACHE == kCacheInt4) int4::quantize<1>(x, word, pair);  // (by the whole warp: it shuffles)
+    if (live && r >= 0 && r < cached) {
       const int h = r - (is_v ? p.num_kv_heads : 0);
       const int64_t page_head = static_cast<int64_t>(page) * p.num_kv_heads + h;
       if (CACHE == kCacheInt4) {
@@ -192,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
         const int64_t at = (page_head * p.page_size + in_page) * kLanes + j;
         uint8_t* pool = is_v ? p.v_pages : p.k_pages;
         if (CACHE == kCacheBf16) {
-          *(reinterpret_cast<uint4*>(pool) + at) = is_v ? in[k] : int4::pack8(x);
+          *(reinterpret_cast<uint4*>(pool) + at) = is_v ? c_row : int4::pack8(x);
         } else {
           const float sc = __ldg((is_v ? p.v_scales : p.k_scales) + h);
           uint2 w;
@@ -203,6 +212,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
       }
     }
     if (!MANY) break;
+    r += stride;
+    c_row = load_cached(r);
   }
 }
 
@@ -215,8 +226,9 @@ cudaError_t launch_rows(RopeAppendParams p, int sms, cudaStream_t stream) {
   if (p.page_size > 1) divisor_magic(static_cast<uint32_t>(p.page_size), &p.ps_magic, &p.ps_shift);
   // As long as all rows fit on the GPU at once, one row a thread: the call's loads are all in flight
   // together.  Beyond that kBatch q rows a thread or more, which finds the token's place, cos and sin once
-  // for all of them.
-  const int64_t per_gpu = int64_t{2048} * sms / (D / 8);
+  // for all of them.  (Into bf16, 32 + 8 heads: 128 tokens 2.7 us one row a thread and 3.5 otherwise, 256
+  // 3.9 and 3.5, 600 7.1 and 5.1; 12 + 2 heads of 64: 800 tokens 3.9 and 4.4, 1200 5.0 and 4.4.)
+  const int64_t per_gpu = int64_t{kThreads * kBlocks} * sms / (D / 8);
   int64_t blocks;
   const bool many = rows > 1 && p.num_tokens * static_cast<int64_t>(rows) > per_gpu;
   if (many) {
