@@ -7,11 +7,10 @@
 // of a channel lies rotary_dim / 16 lanes away: the pair is brought together by shuffles of
 // the packed bf16 words, so no element is read twice.  A thread keeps its cos and sin for all
 // the rows it handles (the same channels of several heads of one token).
-//   Measured: one token of 32 + 8 heads 2.1 us and 256 of them into bf16 3.5 us (the launch, then two
-// dependent loads: position, then block table and angles); 5987 tokens of 12 + 2 heads of 64 into e4m3 6.5
-// us (3.7 TB/s), 16384 of 32 + 8 of 128 into bf16 81 us (5.1 TB/s, 77 % of a copy's rate), of 64 + 8 into 4
-// bits 137 us (4.6 TB/s), where the instructions of the rotation and the quantiser are what is left between
-// it and HBM.
+//   Measured: one token of 32 + 8 heads 2.0 us and 256 of them into bf16 2.9 us (the launch, then two
+// dependent loads: position, then block table and angles); 5987 tokens of 12 + 2 heads of 64 into e4m3 5.6
+// us (4.2 TB/s), 16384 of 32 + 8 of 128 into bf16 70 us (5.8 TB/s, 89 % of a copy's rate), of 64 + 8 into 4
+// bits, the pool read back, 144 us (5.6 TB/s, 85 %).
 #include <climits>
 
 #include <cuda_fp8.h>
@@ -26,9 +25,9 @@ namespace {
 
 constexpr int kThreads = 256;
 // q rows of a thread whose loads are in flight together, and blocks per SM that the registers are held
-// down for: 16384 tokens of 64 + 8 heads into 4 bits with the pool read back take 169 us with (4, 4), 178
-// with (4, 5), 187 with (4, 3), 192 with (3, 4), 167 with (2, 4); of 32 + 8 heads into e4m3 87 us with (4, 4), 98 with
-// (4, 3), 90 with (4, 5); into bf16 81 with (4, 4), 93 with (2, 4).
+// down for: 16384 tokens of 64 + 8 heads into 4 bits with the pool read back take 144 us with (4, 4), 148
+// with (4, 5), 155 with (4, 3), 151 with (3, 4), 154 with (2, 4); of 32 + 8 heads into bf16 70, 75, 78, 74, 77.
+// (A row's successor loaded as soon as it is turned, instead of four at a time: 162 and 80 us.)
 constexpr int kBatch = 4, kBlocks = 4;
 
 __device__ __forceinline__ uint32_t codes2(float a, float b, float s) {
@@ -41,7 +40,7 @@ __device__ __forceinline__ uint32_t codes2(float a, float b, float s) {
 // A token's rows are the q heads, then the k heads, then the v heads.  MANY: 1 << p.spread_log2 q rows
 // of a token are worked on side by side, each thread going on to every such-manieth, and likewise its
 // k and v rows.  Otherwise one row a thread, p.chunks blocks per token.
-template <int D, int CACHE, bool MANY>
+template <int D, int CACHE, bool MANY, bool INTER>
 __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const RopeAppendParams p) {
   // A decode launched right after this one may start its prologue; it waits for this grid
   // before it reads anything that is written here.
@@ -62,18 +61,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
   }
   // The first rows are on their way before it is known where they go, or that they are padding: what a
   // block waits for is latency.  (256 tokens into bf16 4.6 us with
-  // the rows loaded after the page is known, 3.9 so; 16384 of 64 + 8 heads into 4 bits, read back, 182 and 169.)
+  // the rows loaded after the page is known, 3.9 so; 16384 of 64 + 8 heads into 4 bits, read back, 182 and
+  // 169, both before the other steps.)
   const bool here = t < p.num_tokens;
   constexpr int kQ = MANY ? kBatch : 1;
   const int cached = 2 * p.num_kv_heads;
   const uint4* q_in = reinterpret_cast<const uint4*>(p.q + t * p.q_stride) + j;
-  auto load_q = [&](int r0, uint4 (&in)[kQ]) {
-#pragma unroll
-    for (int k = 0; k < kQ; ++k) {
-      in[k] = make_uint4(0, 0, 0, 0);
-      if (here && r0 + k * stride < p.num_heads) in[k] = q_in[(r0 + k * stride) * kLanes];
-    }
-  };
+  auto load_q = [&](int r) { return here && r < p.num_heads ? q_in[r * kLanes] : make_uint4(0, 0, 0, 0); };
   auto load_cached = [&](int r) {
     uint4 in = make_uint4(0, 0, 0, 0);
     if (here && r >= 0 && r < cached) {
@@ -84,7 +78,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
   };
   const int first_cached = MANY ? row : row - p.num_heads;
   uint4 q_rows[kQ];
-  load_q(row, q_rows);
+#pragma unroll
+  for (int k = 0; k < kQ; ++k) q_rows[k] = load_q(row + k * stride);
   uint4 c_row = load_cached(first_cached);
   // (a warp may hold rows of several tokens, of which some are skipped: all its lanes stay for the shuffles)
   bool live = here;
@@ -101,14 +96,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
 
   const int half_lanes = p.rotary_dim / 16;  // lanes of the first half of the rotated channels
   const bool rotated = j < 2 * half_lanes;
-  const bool second = !p.interleaved && j >= half_lanes;
+  const bool second = !INTER && j >= half_lanes;
   // x[i] becomes x[i] c[i] + (its partner) sn[i], the sine's sign taken in; (1, 0) where nothing turns
   float c[8], sn[8];
 #pragma unroll
   for (int m = 0; m < 8; ++m) c[m] = 1.0f, sn[m] = 0.0f;
   if (rotated && live && static_cast<unsigned>(pos) < static_cast<unsigned>(p.max_positions)) {
     const float* at = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim;
-    if (p.interleaved) {  // pairs (2 m, 2 m + 1), m = 4 j .. 4 j + 3
+    if (INTER) {  // pairs (2 m, 2 m + 1), m = 4 j .. 4 j + 3
       const float4 a = __ldg(reinterpret_cast<const float4*>(at) + j);
       const float4 b = __ldg(reinterpret_cast<const float4*>(at + p.rotary_dim / 2) + j);
       c[0] = c[1] = a.x; c[2] = c[3] = a.y; c[4] = c[5] = a.z; c[6] = c[7] = a.w;
@@ -131,11 +126,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
   }
   // the lane that holds the other half of this lane's pairs (itself where nothing is exchanged)
   const int lane = threadIdx.x & 31;
-  const int partner = p.interleaved || !rotated ? lane : (second ? lane - half_lanes : lane + half_lanes);
+  const int partner = INTER || !rotated ? lane : (second ? lane - half_lanes : lane + half_lanes);
   auto rotate = [&](const uint4 in, float (&x)[8]) {
     int4::unpack8(in, x);
     float y[8];
-    if (p.interleaved) {
+    if (INTER) {
 #pragma unroll
       for (int m = 0; m < 8; ++m) y[m] = x[m ^ 1];
     } else {
@@ -163,21 +158,23 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
   // ---- q
   uint4* q_out = reinterpret_cast<uint4*>(p.q_out + static_cast<int64_t>(t) * p.num_heads * D) + j;
 #pragma unroll 1
-  for (int r0 = row; __any_sync(0xffffffffu, r0 < p.num_heads);) {
+  for (int r0 = row; __any_sync(0xffffffffu, r0 < p.num_heads); r0 += kQ * stride) {
 #pragma unroll
     for (int k = 0; k < kQ; ++k) {
+      const int r = r0 + k * stride;
       float x[8];
       rotate(q_rows[k], x);
-      if (live && r0 + k * stride < p.num_heads) q_out[(r0 + k * stride) * kLanes] = int4::pack8(x);
+      if (live && r < p.num_heads) q_out[r * kLanes] = int4::pack8(x);
     }
     if (!MANY) break;
-    r0 += kQ * stride;
-    load_q(r0, q_rows);
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) q_rows[k] = load_q(r0 + (kQ + k) * stride);
   }
 
   // ---- k, then v
 #pragma unroll 1
   for (int r = first_cached; __any_sync(0xffffffffu, r >= 0 && r < cached);) {
+    const uint4 next = MANY ? load_cached(r + stride) : make_uint4(0, 0, 0, 0);
     const bool is_v = r >= p.num_kv_heads;
     float x[8], turned[8];
     int4::unpack8(c_row, x);
@@ -213,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
     }
     if (!MANY) break;
     r += stride;
-    c_row = load_cached(r);
+    c_row = next;
   }
 }
 
@@ -226,14 +223,19 @@ cudaError_t launch_rows(RopeAppendParams p, int sms, cudaStream_t stream) {
   if (p.page_size > 1) divisor_magic(static_cast<uint32_t>(p.page_size), &p.ps_magic, &p.ps_shift);
   // As long as all rows fit on the GPU at once, one row a thread: the call's loads are all in flight
   // together.  Beyond that kBatch q rows a thread or more, which finds the token's place, cos and sin once
-  // for all of them.  (Into bf16, 32 + 8 heads: 128 tokens 2.7 us one row a thread and 3.5 otherwise, 256
-  // 3.9 and 3.5, 600 7.1 and 5.1; 12 + 2 heads of 64: 800 tokens 3.9 and 4.4, 1200 5.0 and 4.4.)
+  // for all of them.  (Into bf16, 32 + 8 heads: 128 tokens 2.8 us one row a thread and 3.0 otherwise, 256
+  // 3.7 and 3.1, 600 6.3 and 4.4; 12 + 2 heads of 64: 400 tokens 2.5 and 3.5, 800 3.9 and 3.6.)
   const int64_t per_gpu = int64_t{kThreads * kBlocks} * sms / (D / 8);
   int64_t blocks;
   const bool many = rows > 1 && p.num_tokens * static_cast<int64_t>(rows) > per_gpu;
   if (many) {
+    // Twice kBatch rows a thread while that leaves the GPU half full of threads: 16384 tokens of 32 + 8
+    // heads into bf16 71 us, and 77 with kBatch; 5987 of 12 + 2 heads of 64 into e4m3 8.1, and 6.4.
     p.spread_log2 = 0;
-    while ((2 << p.spread_log2) <= kSlots && (2 << p.spread_log2) * kBatch <= p.num_heads) ++p.spread_log2;
+    auto can = [&](int rows) { return (2 << p.spread_log2) <= kSlots && (2 << p.spread_log2) * rows <= p.num_heads; };
+    while (can(2 * kBatch)) ++p.spread_log2;
+    if (static_cast<int64_t>(p.num_tokens) * (D / 8 << p.spread_log2) < int64_t{kThreads * kBlocks / 2} * sms)
+      while (can(kBatch)) ++p.spread_log2;
     const int tokens = kSlots >> p.spread_log2;
     blocks = (static_cast<int64_t>(p.num_tokens) + tokens - 1) / tokens;
   } else {
@@ -241,10 +243,9 @@ cudaError_t launch_rows(RopeAppendParams p, int sms, cudaStream_t stream) {
     blocks = static_cast<int64_t>(p.num_tokens) * p.chunks;
   }
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  if (many)
-    rope_append_kernel<D, CACHE, true><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
-  else
-    rope_append_kernel<D, CACHE, false><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+  const auto kernel = p.interleaved ? (many ? rope_append_kernel<D, CACHE, true, true> : rope_append_kernel<D, CACHE, false, true>)
+                                    : (many ? rope_append_kernel<D, CACHE, true, false> : rope_append_kernel<D, CACHE, false, false>);
+  kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
