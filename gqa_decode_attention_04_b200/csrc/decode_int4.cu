@@ -22,9 +22,9 @@
 // Bound: HBM at small groups on paper -- 9/8 D bytes per token and kv head -- but in fact the
 // instructions that turn codes into MMA operands, whatever the number of query rows: about 320 per
 // tile of 16 tokens and row tile, two thirds of them on the integer pipe at half rate.  4 sequences of
-// 131072 tokens, 8 kv heads, 8 rows each: 136 us (4.4 TB/s, 68 % of a copy's rate), 133 with the pool in L2,
-// 107 with the copies alone.  256 sequences of 1 to 32768 tokens: 183 us (5.1 TB/s, 78 %).  More rows
-// widen each tile again for every 16: 96 rows (64 sequences of 8192 tokens, one kv head) 145 us, 0.18
+// 131072 tokens, 8 kv heads, 8 rows each: 130 us (4.6 TB/s, 71 % of a copy's rate), 107 with the copies
+// alone.  256 sequences of 1 to 32768 tokens: 176 us (5.3 TB/s, 81 %).  More rows
+// widen each tile again for every 16: 96 rows (64 sequences of 8192 tokens, one kv head) 144 us, 0.18
 // PFLOP/s.
 //
 // Work.  The list of units (sequence, kv head, row tile, 32 tokens), in that order, is cut into one
@@ -215,12 +215,12 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     for (int w = 0; w < kWarps; ++w) total += scan[w];
     split.total = total * segs;
     // Least work of a warp.  Few long segments are not cut into more than is merged in the time that it
-    // saves: a unit takes 0.8 us, a warp merges four CTAs' parts of a segment in 1 us, and n units a
-    // segment in ranges of x make n / 8 x parts: x = sqrt(n / 26).  (One sequence of 131072 tokens and one
-    // kv head: 31 us, and 63 cut as finely as there are warps; three of 30000 24 and 32.)  A batch of a few
+    // saves: a unit takes 0.8 us, a warp merges eight CTAs' parts of a segment in 1 us, and n units a
+    // segment in ranges of x make n / 8 x parts: x = sqrt(n / 52).  (One sequence of 131072 tokens and one
+    // kv head: 27 us, and 63 cut as finely as there are warps; three of 30000 19 and 32.)  A batch of a few
     // units is not cut finer than a segment of one: two sequences of 17 and 40 tokens take 6.2 us whole
     // and 7.9 cut.
-    int64_t least = static_cast<int64_t>(sqrtf(__fdividef(static_cast<float>(split.total), 26.0f * segs * p.num_seqs)));
+    int64_t least = static_cast<int64_t>(sqrtf(__fdividef(static_cast<float>(split.total), 52.0f * segs * p.num_seqs)));
     least = max(least, split.total <= 4 * kWarps ? int64_t{kSegCost + 1} : int64_t{1});
     split.workers = min(static_cast<int64_t>(gridDim.x) * kWarps, quotient(split.total + least - 1, least));
     split.per = split.total == 0 ? 0 : quotient(split.total, split.workers);
@@ -756,69 +756,61 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     return p.out + ((static_cast<int64_t>(b) * p.q_len + tok) * p.num_heads + static_cast<int64_t>(head) * p.group +
                     (row - tok * p.group)) * D;
   };
-  static_assert(kWarps * C::kRecFloats * 4 <= C::kSmem, "a part per warp beside one another");
-  static_assert(C::kRows <= 4 * kWarps, "a warp has four rows of a segment at most");
   constexpr int kMl = C::kRows * D;  // (reference, sum) of the rows, behind the rows
   const int col = 4 * (lane % (D / 4));
-  // Merges rows r0 .. r0 + 3 of a segment's records -- record_of(i), i < count, of the first 16 only
-  // those with bit i of `some` set -- into their output rows, or into the rows of `into`.  Lane i
-  // looks after records i % 16 of 16, rows r0 + i / 16 and two further; four records of four rows are
-  // loaded at a time, since what a merge waits for is the way to L2.
+  // Rows of a merge, and records whose rows are loaded at a time (what a merge waits for is the way to L2,
+  // but each costs its instructions where there are fewer): 32 sequences of 512 to 4096 tokens take 33.5 us
+  // with (2, 4), 33.3 with (1, 4), 34.2 with (2, 6), 36.0 with (4, 4); with four query tokens 46.9, 50.5, 47.8,
+  // 47.4; 4 of 131072 130.2, 130.6, 130.9, 136.
+  constexpr int MR = 2, kFlight = 4;
+  // Merges rows r0 .. r0 + MR - 1 (of `rows`) of a segment's records -- record_of(i), i < count, of the
+  // first 16 only those with bit i of `some` set -- into their output rows, or into the rows of `into`.
+  // Lane i looks after record i % 16 of 16, of row r0 + i / 16.
   auto merge = [&](int b, int seg, int r0, int rows, int count, uint32_t some, auto record_of, auto load2, auto load4, float* into) {
-    float top[2] = {kNone, kNone}, sum[2] = {0.0f, 0.0f};
-    float4 acc[4];
+    float top = kNone, sum = 0.0f;
+    float4 acc[MR];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int valid = min(4, rows - r0);
+    for (int k = 0; k < MR; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int my_row = r0 + lane / 16;
 #pragma unroll 1
     for (int c = 0; c < count; c += 16) {
       const int i0 = lane & 15;
       const bool mine = c + i0 < count && (some >> i0 & 1);
-      const float* rec = mine ? record_of(c + i0) : nullptr;
-      float a[2], before[2];
-      float2 ml[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = lane / 16 + 2 * j;
-        ml[j] = make_float2(kNone, 0.0f);
-        if (mine && r < valid) ml[j] = load2(rec + kMl + 2 * (r0 + r));
-      }
+      float2 ml = make_float2(kNone, 0.0f);
+      if (mine && my_row < rows) ml = load2(record_of(c + i0) + kMl + 2 * my_row);
       uint32_t todo = __ballot_sync(0xffffffffu, mine) & 0xffffu;
+      float a = 0.0f;
       bool weighed = false;
 #pragma unroll 1
       while (todo) {
-        float4 y[4][4];
-        int from[4];
+        float4 y[kFlight][MR];
+        int from[kFlight];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kFlight; ++q) {
           from[q] = todo ? __ffs(todo) - 1 : -1;
           todo &= todo - 1;
-          const float* at = reinterpret_cast<const float*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rec), max(0, from[q])));
+          const float* rec = record_of(c + max(0, from[q])) + r0 * D + col;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < MR; ++k) {
             y[q][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (from[q] >= 0 && k < valid) y[q][k] = load4(at + (r0 + k) * D + col);
+            if (from[q] >= 0 && (k == 0 || r0 + k < rows)) y[q][k] = load4(rec + k * D);
           }
         }
         if (!weighed) {  // (after the first loads are on their way)
           weighed = true;
+          float now = fmaxf(top, ml.x);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float now = fmaxf(top[j], ml[j].x);
+          for (int d = 1; d < 16; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+          const float before = ptx::ex2(top - now);
+          a = ptx::ex2(ml.x - now);
+          top = now;
+          float part = a * ml.y;
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
-            before[j] = ptx::ex2(top[j] - now);
-            a[j] = ptx::ex2(ml[j].x - now);
-            top[j] = now;
-            float part = a[j] * ml[j].y;
+          for (int d = 1; d < 16; d <<= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+          sum = fmaf(sum, before, part);
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-            sum[j] = fmaf(sum[j], before[j], part);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float f = __shfl_sync(0xffffffffu, before[k / 2], 16 * (k % 2));
+          for (int k = 0; k < MR; ++k) {
+            const float f = __shfl_sync(0xffffffffu, before, 16 * k);
             acc[k].x *= f;
             acc[k].y *= f;
             acc[k].z *= f;
@@ -826,10 +818,10 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           }
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < kFlight; ++q)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float w = __shfl_sync(0xffffffffu, a[k / 2], 16 * (k % 2) + max(0, from[q]));
+          for (int k = 0; k < MR; ++k) {
+            float w = __shfl_sync(0xffffffffu, a, 16 * k + max(0, from[q]));
             if (from[q] < 0) w = 0.0f;
             acc[k].x = fmaf(w, y[q][k].x, acc[k].x);
             acc[k].y = fmaf(w, y[q][k].y, acc[k].y);
@@ -839,27 +831,26 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
       }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float t = __shfl_sync(0xffffffffu, top[k / 2], 16 * (k % 2));
-      const float l = __shfl_sync(0xffffffffu, sum[k / 2], 16 * (k % 2));
-      if (k < valid) {
-        if (into == nullptr) {
-          if (lane < D / 4) st_bf16x4(out_row(b, seg, r0 + k) + col, acc[k], l != 0.0f ? 1.0f / l : 0.0f);
-        } else {
-          if (lane < D / 4) *reinterpret_cast<float4*>(into + (r0 + k) * D + col) = acc[k];
-          if (lane == 0) *reinterpret_cast<float2*>(into + kMl + 2 * (r0 + k)) = make_float2(t, l);
-        }
+    for (int k = 0; k < MR; ++k) {
+      const float t = __shfl_sync(0xffffffffu, top, 16 * k);
+      const float l = __shfl_sync(0xffffffffu, sum, 16 * k);
+      if (k > 0 && r0 + k >= rows) break;
+      if (into == nullptr) {
+        if (lane < D / 4) st_bf16x4(out_row(b, seg, r0 + k) + col, acc[k], l != 0.0f ? 1.0f / l : 0.0f);
+      } else {
+        if (lane < D / 4) *reinterpret_cast<float4*>(into + (r0 + k) * D + col) = acc[k];
+        if (lane == 0) *reinterpret_cast<float2*>(into + kMl + 2 * (r0 + k)) = make_float2(t, l);
       }
     }
   };
   // rows of the segment's row tile
   auto rows_of = [&](int seg) { return min(C::kRows, p.rows - seg % p.n_rt * C::kRows); };
 
-  // over the CTA's warps: lane i looks after piece i; (segment, four rows) go to the warps in turn
+  // over the CTA's warps: lane i looks after piece i; (segment, MR rows) go to the warps in turn
   const int64_t its_start = lane < 2 * kWarps ? pieces[lane].start : 0;
   uint32_t todo = __ballot_sync(0xffffffffu, lane < 2 * kWarps && pieces[lane & (2 * kWarps - 1)].units != 0);
   int outward[2] = {-1, -1};  // pieces whose segment started in an earlier CTA; goes on in a later one
-  int turn = 4 * warp;
+  int turn = MR * warp;
 #pragma unroll 1
   while (todo) {
     const int i = __ffs(todo) - 1;
@@ -870,13 +861,12 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     const int slot = pc.start < cta_start ? 0 : 1;
     if (!inside) outward[slot] = i;
     float* into = inside ? nullptr : p.slots + (2 * static_cast<int64_t>(blockIdx.x) + slot) * C::kRecFloats;
+    const int rows = rows_of(pc.seg);
 #pragma unroll 1
-    for (; turn < C::kRows; turn += 4 * kWarps)
-      if (turn < rows_of(pc.seg))
-        merge(pc.b, pc.seg, turn, rows_of(pc.seg), 2 * kWarps, mine, record,
-              [](const float* x) { return *reinterpret_cast<const float2*>(x); },
-              [](const float* x) { return *reinterpret_cast<const float4*>(x); }, into);
-    turn -= C::kRows;
+    for (; turn < rows; turn += MR * kWarps)
+      merge(pc.b, pc.seg, turn, rows, 2 * kWarps, mine, record, [](const float* x) { return *reinterpret_cast<const float2*>(x); },
+            [](const float* x) { return *reinterpret_cast<const float4*>(x); }, into);
+    turn -= (rows + MR - 1) / MR * MR;
   }
   if (outward[0] < 0 && outward[1] < 0) return;  // (the same in every thread)
 
@@ -906,8 +896,9 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     auto part = [&](int c) { return p.slots + (2 * static_cast<int64_t>(from + c) + (c == 0)) * C::kRecFloats; };
     auto far2 = [](const float* x) { return __ldcg(reinterpret_cast<const float2*>(x)); };
     auto far4 = [](const float* x) { return __ldcg(reinterpret_cast<const float4*>(x)); };
-    const int count = to - from + 1, valid = rows_of(pc.seg), quads = (valid + 3) / 4;
-    if (warp < quads) merge(pc.b, pc.seg, 4 * warp, valid, count, 0xffffu, part, far2, far4, nullptr);
+    const int rows = rows_of(pc.seg);
+#pragma unroll 1
+    for (int r = MR * warp; r < rows; r += MR * kWarps) merge(pc.b, pc.seg, r, rows, to - from + 1, 0xffffu, part, far2, far4, nullptr);
   }
 }
 
