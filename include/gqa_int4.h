@@ -89,7 +89,8 @@ size_t gqa_int4_workspace_bytes(void);
  * which is exact for elements within 2^-28 of the row's largest; the products of the softmax
  * weights with the steps of V are rounded to fp16.  A row whose q holds a non-finite element
  * is NaN.  Slots at or beyond seq_lens[b] and unused pages may hold any bits.
- * Requirements as gqa_paged_decode_attn; q and out 16-byte aligned.
+ * Requirements as gqa_paged_decode_attn; q and out 16-byte aligned; out overlaps no input; num_heads at
+ * most 2^19 - 1.
  */
 gqa_status gqa_paged_decode_attn_int4(const void* q, const void* kv_pages, const int32_t* block_table,
                                       const int32_t* seq_lens, void* out, int num_seqs, int num_heads,

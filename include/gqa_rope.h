@@ -29,7 +29,7 @@
  * The tokens may be one per sequence (a decode step), several (drafts) or whole prompts of
  * different lengths, in any order; no two of them may share a sequence and position (which
  * row is kept, or a mixture of both, is then unspecified).  A row with seq_ids[t] < 0 is
- * padding: skipped, its q_out row left as it was.  A seq_id >= num_seqs, a position outside
+ * padding: skipped (its q, k_new and v_new rows may be read), its q_out row left as it was.  A seq_id >= num_seqs, a position outside
  * [0, max_blocks_per_seq * page_size) or >= max_positions, or a page id outside
  * [0, num_pages) skips the row likewise and sets GQA_ERR_DEVICE_BOUNDS in the device error
  * word.  No other byte of the pools is written.
