@@ -130,7 +130,8 @@ def _load_fast(lib) -> None:
     except ImportError:
         return
     for name in ("gqa_rope_kv_append", "gqa_rope_kv_append_fp8", "gqa_rope_kv_append_int4", "gqa_kv_quantize_int4",
-                 "gqa_kv_dequantize_int4", "gqa_paged_decode_attn_int4", "gqa_paged_multi_query_attn_int4"):
+                 "gqa_kv_dequantize_int4", "gqa_paged_decode_attn_int4", "gqa_paged_multi_query_attn_int4",
+                 "gqa_decode_step_int4"):
         _entry[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
     _fast = _fastcall
 
@@ -903,6 +904,10 @@ def decode_step_int4(q, k_new, v_new, kv_pages, block_table, positions, seq_lens
     With cos_sin (as rope_kv_append), q and k_new are rotated on the way; q_rot, if given, receives
     the rotated q.
     """
+    if (stream is None and out is not None and workspace is not None and (cos_sin is None or q_rot is not None)
+            and _quick("step", "gqa_decode_step_int4", q, k_new, v_new, kv_pages, block_table, positions, seq_lens, cos_sin,
+                       interleaved, q_rot, out, scale, workspace)):
+        return out
     dev = q.device
     _all(dev, (q, "q", torch.bfloat16), (k_new, "k_new", torch.bfloat16), (v_new, "v_new", torch.bfloat16),
          (block_table, "block_table", torch.int32), (positions, "positions", torch.int32),

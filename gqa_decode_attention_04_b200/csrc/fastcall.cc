@@ -1,4 +1,4 @@
-// Marshalling of the 4-bit attention, conversion and rotating-append calls without ctypes: the same
+// Marshalling of the 4-bit attention, step, conversion and rotating-append calls without ctypes: the same
 // checks as the Python binding's, asked of the tensors directly.  Each function calls the library's
 // entry point whose address it is given and returns its status, or None if an argument is not what the
 // call takes; the Python binding then goes its own way, which says what is wrong.  An append, of 25
@@ -154,6 +154,42 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(status);
 }
 
+// step(fn, device, stream, q, k_new, v_new, kv_pages, block_table, positions, seq_lens, cos_sin or None, interleaved,
+//      q_rot (with cos_sin), out, scale, workspace)
+PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  WANT(n == 16);
+  const long dev = PyLong_AsLong(a[1]);
+  void* stream = address(a[2]);
+  const int inter = PyObject_IsTrue(a[11]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor *q = tensor(a[3], kBf16, dev, 3), *k = tensor(a[4], kBf16, dev, 3), *v = tensor(a[5], kBf16, dev, 3),
+                   *pool = tensor(a[6], kByte, dev, 4), *bt = tensor(a[7], kInt, dev, 2), *pos = tensor(a[8], kInt, dev, 1),
+                   *sl = tensor(a[9], kInt, dev, 1), *out = tensor(a[13], kBf16, dev, 3), *ws = tensor(a[15], kByte, dev, 1);
+  WANT(q && k && v && pool && bt && pos && sl && out && ws);
+  const at::Tensor *cs = nullptr, *qr = nullptr;
+  if (a[10] != Py_None) {
+    cs = tensor(a[10], kFloat, dev, 2);
+    qr = tensor(a[12], kBf16, dev, 3);
+    WANT(cs && qr && qr->sizes() == q->sizes());
+  } else {
+    WANT(a[12] == Py_None);
+  }
+  const int64_t seqs = q->size(0), d = q->size(2), Hk = pool->size(1);
+  WANT(pool->size(3) == 18 * d && pool->size(2) <= 256 && k->size(0) == seqs && k->size(1) == Hk && k->size(2) == d &&
+       v->sizes() == k->sizes() && bt->size(0) == seqs && pos->size(0) == seqs && sl->size(0) == seqs && out->sizes() == q->sizes());
+  const double scale = a[14] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : PyFloat_AsDouble(a[14]);
+  if (PyErr_Occurred()) return nullptr;
+  using Fn = int (*)(const void*, const void*, const void*, const void*, void*, void*, const void*, const void*, const void*, void*, int,
+                     int, int, int, int, int, int, int, float, int, int, void*, size_t, void*);
+  const int status = reinterpret_cast<Fn>(address(a[0]))(
+      q->data_ptr(), k->data_ptr(), v->data_ptr(), cs ? cs->data_ptr() : nullptr, qr ? qr->data_ptr() : nullptr, pool->data_ptr(),
+      bt->data_ptr(), pos->data_ptr(), sl->data_ptr(), out->data_ptr(), static_cast<int>(seqs), static_cast<int>(q->size(1)),
+      static_cast<int>(Hk), static_cast<int>(d), cs ? static_cast<int>(cs->size(1)) : 0, inter, cs ? static_cast<int>(cs->size(0)) : 0,
+      static_cast<int>(16 * pool->size(2)), static_cast<float>(scale), static_cast<int>(bt->size(1)),
+      static_cast<int>(pool->size(0)), ws->data_ptr(), static_cast<size_t>(ws->numel()), stream);
+  return PyLong_FromLong(status);
+}
+
 // A tensor without memory, sizes or strides of its own (one that a tracer makes) throws when it is asked
 // for them: it is not what the call takes.
 template <PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)>
@@ -170,6 +206,7 @@ PyMethodDef kMethods[] = {
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<attend>)), METH_FASTCALL, nullptr},
     {"convert", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<convert>)), METH_FASTCALL, nullptr},
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<rope>)), METH_FASTCALL, nullptr},
+    {"step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<step>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

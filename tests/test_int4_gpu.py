@@ -512,3 +512,43 @@ def test_tensors_without_plain_memory_are_refused(cuda_device):
             gq.quantize_pages_int4(pages.to_sparse(), pages, pool)
     torch.cuda.synchronize()
     gq.check_device_error()
+
+
+@pytest.mark.parametrize("rotate", [True, False])
+def test_a_step_with_given_outputs_goes_the_native_way_and_gives_the_same(cuda_device, rotate):
+    rng = np.random.default_rng(61)
+    lens = [60, 33]
+    bt, pages = make_table(rng, lens, 16)
+    pools = [torch.from_numpy(make_pool(rng, pages, 2, 16, 64)).to(cuda_device)]
+    pools.append(pools[0].clone())
+    dbt, dsl = device(cuda_device, bt, np.array(lens, np.int32))
+    q, k, v = (bf16(rng.standard_normal((2, h, 64))).to(cuda_device) for h in (8, 2, 2))
+    cs = torch.from_numpy(rng.standard_normal((100, 32)).astype(np.float32)).to(cuda_device) if rotate else None
+    ws = gq.int4_workspace()
+    args = dict(q=q, k_new=k, v_new=v, block_table=dbt, positions=dsl - 1, seq_lens=dsl, cos_sin=cs, interleaved=rotate)
+    want = gq.decode_step_int4(kv_pages=pools[0], **args)
+    given = dict(out=torch.empty_like(q), q_rot=torch.empty_like(q) if rotate else None, workspace=ws)
+    called = []
+    native = gq._fast.step
+
+    class Counted:
+        def __getattr__(self, name):
+            return getattr(fast, name)
+
+        def step(self, *a):
+            called.append(native(*a))
+            return called[-1]
+
+    fast, gq._fast = gq._fast, Counted()
+    try:
+        assert gq.decode_step_int4(kv_pages=pools[1], **args, **given) is given["out"]
+        assert called == [0]
+        for bad in (dict(q=q[0]), dict(k_new=k[:, :1]), dict(v_new=v.float()), dict(positions=dsl.long()), dict(seq_lens=dsl[:1]),
+                    dict(block_table=dbt[:1]), dict(out=q[:, :4]), dict(workspace=ws[:100].clone()), dict(scale=float("inf")),
+                    dict(q_rot=q[:1]), dict(cos_sin=torch.ones(3, 24, device=cuda_device), q_rot=given["out"])):
+            with pytest.raises((ValueError, TypeError, gq.GQAError)):
+                gq.decode_step_int4(**{**args, "kv_pages": pools[1], **given, **bad})
+    finally:
+        gq._fast = fast
+    assert torch.equal(given["out"], want) and torch.equal(*pools)
+    gq.check_device_error()
