@@ -22,9 +22,9 @@
 // Bound: HBM at small groups on paper -- 9/8 D bytes per token and kv head -- but in fact the
 // instructions that turn codes into MMA operands, whatever the number of query rows: about 320 per
 // tile of 16 tokens and row tile, two thirds of them on the integer pipe at half rate.  4 sequences of
-// 131072 tokens, 8 kv heads, 8 rows each: 130 us (4.6 TB/s, 71 % of a copy's rate), 107 with the copies
+// 131072 tokens, 8 kv heads, 8 rows each: 127 us (4.7 TB/s, 72 % of a copy's rate), 107 with the copies
 // alone.  256 sequences of 1 to 32768 tokens: 176 us (5.3 TB/s, 81 %).  More rows
-// widen each tile again for every 16: 96 rows (64 sequences of 8192 tokens, one kv head) 144 us, 0.18
+// widen each tile again for every 16: 96 rows (64 sequences of 8192 tokens, one kv head) 146 us, 0.18
 // PFLOP/s.
 //
 // Work.  The list of units (sequence, kv head, row tile, 32 tokens), in that order, is cut into one
@@ -37,8 +37,9 @@
 // 42 for 36 on 32 sequences of 512 to 4096 tokens.)  A segment wholly inside a warp's range is written
 // out at once.  What a range cuts is left in shared memory or the workspace (at most the first and the
 // last segment of a warp), merged over the CTA's warps after one __syncthreads, and over CTAs through
-// two workspace slots per CTA: the last CTA to arrive at a segment's counter merges it.  Which order
-// the CTAs arrive in changes nothing: the parts are summed in the order of the list.
+// two workspace slots per CTA: the warp that is last to arrive at the counter of a segment's two rows
+// merges those.  (With a barrier of the CTA and one counter a segment: 33.4 us for 31.8 on that batch.)
+// Which order the CTAs arrive in changes nothing: the parts are summed in the order of the list.
 //
 // The S tile is computed transposed, S^T = K Q^T (tokens on the MMA's 16-row side, 8 query
 // rows on the other), so a group of 4 or 8 heads needs no padding to 16.
@@ -61,6 +62,12 @@ constexpr int kWarps = 8;
 static_assert((2 * kWarps & (2 * kWarps - 1)) == 0 && 2 * kWarps <= 32, "a lane per piece of the CTA");
 constexpr float kNone = -3.0e38f;   // reference of a row that has seen no token
 
+// Rows of a merge, and records whose rows are loaded at a time (what a merge waits for is the way to L2,
+// but each costs its instructions where there are fewer): 32 sequences of 512 to 4096 tokens take 31.7 us
+// with (2, 5), 31.6 with (2, 4), 31.7 with (2, 2), 33.0 with (1, 4); with four query tokens 47.7, 47.8, 46.6,
+// 52.7; 4 of 131072 127.4, 126.5, 128.7, 130.7; 64 of 8192 with 96 heads 146.4, 150, 149.7, 150.4.
+constexpr int kMergeRows = 2, kFlight = 5;
+
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;              // query rows of a segment
@@ -69,6 +76,7 @@ struct Cfg {
   static constexpr int kUnitBytes = 2 * kTileBytes;
   static constexpr int kStages = 3;
   static constexpr int kCtas = NT == 1 ? 2 : 1;     // per SM
+  static constexpr int kCounters = kRows / kMergeRows;  // of a CTA
   static constexpr int kRecFloats = kRows * (D + 2);  // a piece: [rows][D], then (reference, sum)
   static constexpr int kRingBytes = kStages * kUnitBytes;
   static_assert(kRingBytes >= kRecFloats * 4, "the last piece of a warp is left in its ring");
@@ -168,7 +176,6 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   __shared__ int64_t scan[kWarps];
   __shared__ __align__(8) uint64_t full[kWarps][C::kStages];
   __shared__ Piece pieces[2 * kWarps];
-  __shared__ int2 last_of[2];
   __shared__ Split kept;  // for the merges: the loop has no registers for it
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -758,11 +765,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   };
   constexpr int kMl = C::kRows * D;  // (reference, sum) of the rows, behind the rows
   const int col = 4 * (lane % (D / 4));
-  // Rows of a merge, and records whose rows are loaded at a time (what a merge waits for is the way to L2,
-  // but each costs its instructions where there are fewer): 32 sequences of 512 to 4096 tokens take 33.5 us
-  // with (2, 4), 33.3 with (1, 4), 34.2 with (2, 6), 36.0 with (4, 4); with four query tokens 46.9, 50.5, 47.8,
-  // 47.4; 4 of 131072 130.2, 130.6, 130.9, 136.
-  constexpr int MR = 2, kFlight = 4;
+  constexpr int MR = kMergeRows;
   // Merges rows r0 .. r0 + MR - 1 (of `rows`) of a segment's records -- record_of(i), i < count, of the
   // first 16 only those with bit i of `some` set -- into their output rows, or into the rows of `into`.
   // Lane i looks after record i % 16 of 16, of row r0 + i / 16.
@@ -846,10 +849,11 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   // rows of the segment's row tile
   auto rows_of = [&](int seg) { return min(C::kRows, p.rows - seg % p.n_rt * C::kRows); };
 
-  // over the CTA's warps: lane i looks after piece i; (segment, MR rows) go to the warps in turn
+  // Lane i looks after piece i; (segment, MR rows) go to the warps in turn: first what the CTA has of the
+  // rows, then, where the segment goes on in other CTAs, the arrival at their counter.  The last CTA's warp to
+  // arrive merges those rows' parts, so no warp waits for another, nor for other rows.
   const int64_t its_start = lane < 2 * kWarps ? pieces[lane].start : 0;
   uint32_t todo = __ballot_sync(0xffffffffu, lane < 2 * kWarps && pieces[lane & (2 * kWarps - 1)].units != 0);
-  int outward[2] = {-1, -1};  // pieces whose segment started in an earlier CTA; goes on in a later one
   int turn = MR * warp;
 #pragma unroll 1
   while (todo) {
@@ -858,47 +862,31 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     const uint32_t mine = todo & __ballot_sync(0xffffffffu, its_start == pc.start);
     todo &= ~mine;
     const bool inside = pc.start >= cta_start && pc.start + pc.units <= cta_end;
-    const int slot = pc.start < cta_start ? 0 : 1;
-    if (!inside) outward[slot] = i;
+    const int slot = pc.start < cta_start ? 0 : 1;  // it started in an earlier CTA; it goes on in a later one
     float* into = inside ? nullptr : p.slots + (2 * static_cast<int64_t>(blockIdx.x) + slot) * C::kRecFloats;
     const int rows = rows_of(pc.seg);
 #pragma unroll 1
-    for (; turn < rows; turn += MR * kWarps)
+    for (; turn < rows; turn += MR * kWarps) {
       merge(pc.b, pc.seg, turn, rows, 2 * kWarps, mine, record, [](const float* x) { return *reinterpret_cast<const float2*>(x); },
             [](const float* x) { return *reinterpret_cast<const float4*>(x); }, into);
-    turn -= (rows + MR - 1) / MR * MR;
-  }
-  if (outward[0] < 0 && outward[1] < 0) return;  // (the same in every thread)
-
-  // over CTAs
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    int2 ctas = make_int2(0, -1);  // empty unless this CTA is the last to arrive
-    const int i = outward[threadIdx.x];
-    if (i >= 0) {
-      const Piece pc = pieces[i];
+      if (inside) continue;
       const int from = static_cast<int>(kept.owner(pc.start) / kWarps);
       const int to = static_cast<int>(kept.owner(pc.start + pc.units - 1) / kWarps);
-      if (atomicAdd(p.counters + from, 1) == to - from) ctas = make_int2(from, to);
+      int32_t* counter = p.counters + from * C::kCounters + turn / MR;
+      __threadfence();
+      __syncwarp();
+      int last = 0;
+      if (lane == 0) last = atomicAdd(counter, 1) == to - from;
+      if (__shfl_sync(0xffffffffu, last, 0) == 0) continue;
+      __threadfence();
+      if (lane == 0) *counter = 0;
+      // the first CTA's part is its second slot, the others' their first
+      merge(pc.b, pc.seg, turn, rows, to - from + 1, 0xffffu,
+            [&](int c) { return p.slots + (2 * static_cast<int64_t>(from + c) + (c == 0)) * C::kRecFloats; },
+            [](const float* x) { return __ldcg(reinterpret_cast<const float2*>(x)); },
+            [](const float* x) { return __ldcg(reinterpret_cast<const float4*>(x)); }, nullptr);
     }
-    last_of[threadIdx.x] = ctas;
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int k = 0; k < 2; ++k) {
-    const int from = last_of[k].x, to = last_of[k].y;
-    if (to < from) continue;
-    __threadfence();
-    const Piece pc = pieces[outward[k]];
-    if (threadIdx.x == 0) p.counters[from] = 0;
-    // the first CTA's part is its second slot, the others' their first
-    auto part = [&](int c) { return p.slots + (2 * static_cast<int64_t>(from + c) + (c == 0)) * C::kRecFloats; };
-    auto far2 = [](const float* x) { return __ldcg(reinterpret_cast<const float2*>(x)); };
-    auto far4 = [](const float* x) { return __ldcg(reinterpret_cast<const float4*>(x)); };
-    const int rows = rows_of(pc.seg);
-#pragma unroll 1
-    for (int r = MR * warp; r < rows; r += MR * kWarps) merge(pc.b, pc.seg, r, rows, to - from + 1, 0xffffu, part, far2, far4, nullptr);
+    turn -= (rows + MR - 1) / MR * MR;
   }
 }
 
@@ -907,7 +895,8 @@ namespace {
 template <int D, int NT>
 Int4Plan plan_of() {
   using C = Cfg<D, NT>;
-  return {NT, kWarps, C::kCtas, static_cast<size_t>(C::kSmem), static_cast<size_t>(C::kRecFloats) * (C::kRecHere ? 2 : 2 + kWarps) * sizeof(float)};
+  return {NT, kWarps, C::kCtas, static_cast<size_t>(C::kSmem), static_cast<size_t>(C::kRecFloats) * (C::kRecHere ? 2 : 2 + kWarps) * sizeof(float),
+          kInt4Counters / C::kCounters};
 }
 
 template <int D, int NT>

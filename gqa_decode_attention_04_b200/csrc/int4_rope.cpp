@@ -183,13 +183,13 @@ gqa_status decode(const void* q, const void* kv_pages, const int32_t* block_tabl
   s = gqa::host_device(&p.err, &sms);
   if (s != GQA_OK) return s;
   const gqa::Knobs knobs = gqa::host_knobs();
-  constexpr size_t kHeader = gqa::kInt4MaxCtas * sizeof(int32_t);
+  constexpr size_t kHeader = gqa::kInt4Counters * sizeof(int32_t);
   const int64_t fit = static_cast<int64_t>((GQA_INT4_WORKSPACE_BYTES - kHeader) / plan.slot_bytes);
   // no more CTAs than the longest lengths could keep busy (the lengths are device data)
   const int64_t tiles = static_cast<int64_t>(num_seqs) * num_kv_heads * n_rt *
                         (static_cast<int64_t>(max_blocks) * (page_size / kTile));
   int64_t grid = knobs.workers > 0 ? knobs.workers : static_cast<int64_t>(sms) * plan.ctas_per_sm;
-  const int64_t limits[] = {fit, gqa::kInt4MaxCtas, (tiles + plan.warps - 1) / plan.warps};
+  const int64_t limits[] = {fit, plan.max_ctas, (tiles + plan.warps - 1) / plan.warps};
   for (const int64_t limit : limits)
     if (grid > limit) grid = limit;
 

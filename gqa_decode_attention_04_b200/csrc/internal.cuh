@@ -151,7 +151,7 @@ struct Int4DecodeParams {
   const uint8_t* pool;        // [P, Hk, ps / 16, 18 D]
   const int32_t* block_table; // [B, MB]
   const int32_t* seq_lens;    // [B]
-  int32_t* counters;          // [kInt4MaxCtas], zero between launches
+  int32_t* counters;          // [kInt4Counters], zero between launches
   float* slots;               // two per CTA, then one per warp: [rows][D] sums, then [rows][2] (reference, sum)
   uint32_t* err;
   int num_seqs, num_heads, num_kv_heads, group, q_len;
@@ -164,13 +164,14 @@ struct Int4DecodeParams {
   uint32_t tpp_magic;         // division by tiles_per_page (divisor_magic); 0: by 1
   int tpp_shift;
 };
-constexpr int kInt4MaxCtas = 4096;
+constexpr int kInt4Counters = 4096;
 struct Int4Plan {
   int n_tiles;        // 8-row MMA tiles of a warp
   int warps;          // of a CTA
   int ctas_per_sm;
   size_t smem_bytes;
   size_t slot_bytes;  // of one CTA
+  int max_ctas;       // for which there are counters
 };
 Int4Plan plan_decode_int4(int head_dim, int rows);
 cudaError_t launch_decode_int4(const Int4DecodeParams& p, const Int4Plan& plan, int head_dim, int grid,
