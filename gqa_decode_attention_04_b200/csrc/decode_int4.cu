@@ -895,7 +895,7 @@ namespace {
 template <int D, int NT>
 Int4Plan plan_of() {
   using C = Cfg<D, NT>;
-  return {NT, kWarps, C::kCtas, static_cast<size_t>(C::kSmem), static_cast<size_t>(C::kRecFloats) * (C::kRecHere ? 2 : 2 + kWarps) * sizeof(float),
+  return {NT, kWarps, C::kCtas, static_cast<size_t>(C::kRecFloats) * (C::kRecHere ? 2 : 2 + kWarps) * sizeof(float),
           kInt4Counters / C::kCounters};
 }
 

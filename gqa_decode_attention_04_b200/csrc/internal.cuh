@@ -169,7 +169,6 @@ struct Int4Plan {
   int n_tiles;        // 8-row MMA tiles of a warp
   int warps;          // of a CTA
   int ctas_per_sm;
-  size_t smem_bytes;
   size_t slot_bytes;  // of one CTA
   int max_ctas;       // for which there are counters
 };
