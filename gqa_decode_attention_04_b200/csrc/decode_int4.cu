@@ -12,7 +12,9 @@
 // nibbles' channels of q are scaled by 2^-4) and into the output (for V).
 //   q is scaled by a power of two per row so that its largest element lies in [2^14, 2^15):
 // exact in fp16 for elements within 2^-28 of it (bf16 has 8 significant bits), and the products
-// with c * 2^-24 stay normal in fp32.
+// with c * 2^-24 stay normal in fp32.  Any finite q has such a power.  A score in the units of these products,
+// the sum over g above times 2^(e - 24), is some 2^-9 |k|: the tensor core may drop what of the minima's part
+// lies below 2^-126, which is 2^-126 scale log2(e) 2^(24 - e) < 2^-15 of a score while |scale q| < 2^100.
 //   The minima's part of a score is one more MMA of depth 4 per tile, in tf32: m is exact there, and
 // sum(q_g) goes in as two parts of 11 bits.
 //   p s is rounded to fp16.  Steps may be of any size, so each row carries a power of two F that
@@ -379,38 +381,46 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) {
           int4::unpack8(w[i], x[i]);
-          if (i % 2 == 0) sum[i / 2] = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            top = int4::max_nan(top, fabsf(x[i][e]));
-            sum[i / 2] += x[i][e];
-          }
+          for (int e = 0; e < 8; ++e) top = int4::max_nan(top, fabsf(x[i][e]));
         }
         top = int4::max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = int4::max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // up = 2^e with top * 2^e in [2^14, 2^15), for every finite top down to 2^-112 (a smaller one, a multiple
+        // of bf16's least number, is exact all the same).  The sums are taken after it: they stay finite.
+        const int top_e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        const int e = min(126, 14 - top_e);  // -114 (not finite) and above
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) {
+          if (i % 2 == 0) sum[i / 2] = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            x[i][c] *= up;
+            sum[i / 2] += x[i][c];
+          }
+        }
 #pragma unroll
         for (int u = 0; u < G; ++u) {
           sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 1);
           sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 2);
         }
-        // up = 2^e with top * 2^e in [2^14, 2^15), |e| <= 100
-        const int top_e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        const int e = max(-100, min(100, 14 - top_e));
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        float down = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 24 - e) << 23);
+        // scale log2(e) 2^(24 - e); the power in two factors, as it may pass fp32's range where the product does not
+        const int e0 = (24 - e) >> 1, e1 = 24 - e - e0;
+        float down = p.scale * __uint_as_float(static_cast<uint32_t>(127 + e0) << 23) * 1.4426950408889634f *
+                     __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
         if (!(top < INFINITY)) down = __uint_as_float(0x7fffffffu);  // the row is NaN
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) {
-          float* y = x[i];
-          const float up4 = up * 0.0625f;
-          qf[nt][2 * i][0] = ptx::pack_f16x2(y[0] * up, y[4] * up);
-          qf[nt][2 * i][1] = ptx::pack_f16x2(y[1] * up4, y[5] * up4);
-          qf[nt][2 * i + 1][0] = ptx::pack_f16x2(y[2] * up, y[6] * up);
-          qf[nt][2 * i + 1][1] = ptx::pack_f16x2(y[3] * up4, y[7] * up4);
+          const float* y = x[i];
+          qf[nt][2 * i][0] = ptx::pack_f16x2(y[0], y[4]);
+          qf[nt][2 * i][1] = ptx::pack_f16x2(y[1] * 0.0625f, y[5] * 0.0625f);
+          qf[nt][2 * i + 1][0] = ptx::pack_f16x2(y[2], y[6]);
+          qf[nt][2 * i + 1][1] = ptx::pack_f16x2(y[3] * 0.0625f, y[7] * 0.0625f);
         }
         // The sum of q in the units of the codes' products, cut into two parts of 11 bits, which
         // tf32 holds exactly: the minima (bf16) times them lose 2^-22 at most.
-        const float mine = (G == 2 && (t & 1) ? sum[G - 1] : sum[0]) * up * 0x1p-24f;
+        const float mine = (G == 2 && (t & 1) ? sum[G - 1] : sum[0]) * 0x1p-24f;
         const float upper = __uint_as_float(__float_as_uint(mine) & 0xffffe000u);
         const float lower = __uint_as_float(__float_as_uint(mine - upper) & 0xffffe000u);
         qsum[nt] = __float_as_uint(t / G == 0 ? upper : (t / G == 1 ? lower : 0.0f));

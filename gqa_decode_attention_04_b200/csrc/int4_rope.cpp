@@ -211,7 +211,7 @@ gqa_status decode(const void* q, const void* kv_pages, const int32_t* block_tabl
   p.tiles_per_page = page_size / kTile;
   p.max_blocks = max_blocks;
   p.num_pages = num_pages;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale = scale;
   p.wait_limit_ns = knobs.wait_limit_ns;
   p.arm_without_copy = knobs.arm_without_copy;
   if (p.tiles_per_page > 1) gqa::divisor_magic(static_cast<uint32_t>(p.tiles_per_page), &p.tpp_magic, &p.tpp_shift);

@@ -158,7 +158,7 @@ struct Int4DecodeParams {
   int rows;                   // query rows per kv head: group * q_len
   int n_rt;                   // row tiles (segments) per kv head
   int page_size, tiles_per_page, max_blocks, num_pages;
-  float scale_log2;           // scale * log2(e)
+  float scale;
   uint64_t wait_limit_ns;
   int arm_without_copy;
   uint32_t tpp_magic;         // division by tiles_per_page (divisor_magic); 0: by 1

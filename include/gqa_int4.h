@@ -87,8 +87,10 @@ size_t gqa_int4_workspace_bytes(void);
  *
  * Scores and sums are held in fp32.  q is scaled by a power of two per row and held in fp16,
  * which is exact for elements within 2^-28 of the row's largest; the products of the softmax
- * weights with the steps of V are rounded to fp16.  A row whose q holds a non-finite element
- * is NaN.  Slots at or beyond seq_lens[b] and unused pages may hold any bits.
+ * weights with the steps of V are rounded to fp16.  A row that sees a token and whose q holds a
+ * non-finite element is NaN.  Slots at or beyond seq_lens[b] and unused pages may hold any bits.
+ * Range: q, K and scale of any finite size with |scale * q| < 2^100 for every element of q and
+ * scores, |scale| * sum |q| |k|, within fp32's range; beyond it an output may be anything.
  * Requirements as gqa_paged_decode_attn; q and out 16-byte aligned; out overlaps no input; num_heads at
  * most 2^19 - 1.
  */
