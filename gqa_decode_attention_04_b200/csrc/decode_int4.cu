@@ -707,14 +707,13 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           const float inv = l[nt][c] != 0.0f ? 1.0f / l[nt][c] : 0.0f;  // NaN stays NaN
 #pragma unroll
           for (int u = 0; u < G; ++u) {
-            // 1 / F: a power of two in [2^-126, 2^126]
+            // 1 / F: a power of two in [2^-126, 2^126], so it does not take the codes' 2^24 as well
             const float over = __uint_as_float((254u << 23) - __float_as_uint(F[nt][c]));
-            const float even = 0x1p24f * over, odd = 0x1p20f * over;
             float y[8];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-              y[2 * m] = fmaf(o[4 * u + m][nt][c], even, pm[nt][u][c]);
-              y[2 * m + 1] = fmaf(o[4 * u + m][nt][c + 2], odd, pm[nt][u][c]);
+              y[2 * m] = fmaf(o[4 * u + m][nt][c] * 0x1p24f, over, pm[nt][u][c]);
+              y[2 * m + 1] = fmaf(o[4 * u + m][nt][c + 2] * 0x1p20f, over, pm[nt][u][c]);
             }
             if (whole) {
               if (row0 + r < p.rows) {

@@ -90,7 +90,8 @@ size_t gqa_int4_workspace_bytes(void);
  * weights with the steps of V are rounded to fp16.  A row that sees a token and whose q holds a
  * non-finite element is NaN.  Slots at or beyond seq_lens[b] and unused pages may hold any bits.
  * Range: q, K and scale of any finite size with |scale * q| < 2^100 for every element of q and
- * scores, |scale| * sum |q| |k|, within fp32's range; beyond it an output may be anything.
+ * scores, |scale| * sum |q| |k|, within fp32's range; V with |v| times the number of tokens up to
+ * 2^115.  Beyond it an output may be anything.
  * Requirements as gqa_paged_decode_attn; q and out 16-byte aligned; out overlaps no input; num_heads at
  * most 2^19 - 1.
  */

@@ -74,3 +74,16 @@ def test_sizes_of_q_k_and_v(cuda_device, size, heads):
     assert scale * float(q.abs().max()) < 2.0 ** 100
     for s, workers in ((scale, 2), (-0.7 * scale, 0)):
         attend(cuda_device, q, k, v, bt, lens, s, workers)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_largest_values_of_v(cuda_device, D):
+    """|v| times the number of tokens up to 2^115."""
+    rng = np.random.default_rng(D)
+    lens, ps = [20, 7, 1], 16
+    bt, pages = make_table(rng, lens, ps)
+    k = rng.standard_normal((pages, 2, ps, D)).astype(np.float32)
+    v = rng.uniform(-1.0, 1.0, (pages, 2, ps, D)).astype(np.float32) * np.float32(2.0 ** 115 / 20)
+    for Q in (1, 4):
+        q = bf16(rng.standard_normal((3, 8, D) if Q == 1 else (3, Q, 8, D)))
+        attend(cuda_device, q, k, v, bt, lens, D ** -0.5)
