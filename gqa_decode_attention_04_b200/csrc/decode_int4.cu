@@ -18,7 +18,8 @@
 //   The minima's part of a score is one more MMA of depth 4 per tile, in tf32: m is exact there, and
 // sum(q_g) goes in as two parts of 11 bits.
 //   p s is rounded to fp16.  Steps may be of any size, so each row carries a power of two F that
-// keeps p s F below 2^15; it moves with the running maximum, which itself moves only when a score
+// keeps p s F below 2^15 (F is 2^115 at most, so steps below 2^-112 lose bits: 2^-25 / F = 2^-140 absolutely for
+// each token's weight); it moves with the running maximum, which itself moves only when a score
 // passes it by 2^12.  Scores, sums and outputs are fp32.
 //
 // Bound: HBM at small groups on paper -- 9/8 D bytes per token and kv head -- but in fact the
@@ -156,11 +157,11 @@ __device__ __forceinline__ void st_bf16x4(uint16_t* dst, const float4& o, float 
   *reinterpret_cast<uint2*>(dst) = w;
 }
 
-// 2^-floor(log2 m) for m > 0 (finite), between 2^-126 and 2^126; 2^100 for 0 or less.
+// 2^-floor(log2 m) for finite m, between 2^-126 and 2^115 (which 0 gives, too).  Not more: times a weight of up to
+// 2^12, before it meets a step that may be 0, it has to be finite.
 __device__ __forceinline__ float inverse_pow2(float m) {
-  if (!(m > 0.0f)) return 0x1p100f;
   int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;  // (a subnormal counts as 2^-127)
-  e = max(-126, min(126, e));
+  e = max(-115, min(126, e));
   return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
@@ -707,7 +708,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
           const float inv = l[nt][c] != 0.0f ? 1.0f / l[nt][c] : 0.0f;  // NaN stays NaN
 #pragma unroll
           for (int u = 0; u < G; ++u) {
-            // 1 / F: a power of two in [2^-126, 2^126], so it does not take the codes' 2^24 as well
+            // 1 / F: a power of two in [2^-115, 2^126], so it does not take the codes' 2^24 as well
             const float over = __uint_as_float((254u << 23) - __float_as_uint(F[nt][c]));
             float y[8];
 #pragma unroll

@@ -91,7 +91,8 @@ size_t gqa_int4_workspace_bytes(void);
  * non-finite element is NaN.  Slots at or beyond seq_lens[b] and unused pages may hold any bits.
  * Range: q, K and scale of any finite size with |scale * q| < 2^100 for every element of q and
  * scores, |scale| * sum |q| |k|, within fp32's range; V with |v| times the number of tokens up to
- * 2^115.  Beyond it an output may be anything.
+ * 2^115.  Beyond it an output may be anything.  Values of V below 2^-110 are off by up to 2^-136
+ * absolutely per token that a row sees.
  * Requirements as gqa_paged_decode_attn; q and out 16-byte aligned; out overlaps no input; num_heads at
  * most 2^19 - 1.
  */

@@ -87,3 +87,21 @@ def test_the_largest_values_of_v(cuda_device, D):
     for Q in (1, 4):
         q = bf16(rng.standard_normal((3, 8, D) if Q == 1 else (3, Q, 8, D)))
         attend(cuda_device, q, k, v, bt, lens, D ** -0.5)
+
+
+@pytest.mark.parametrize("rise,size", [(4.0, 1e-36), (8.0, 1e-35)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_row_of_zeros_behind_tiny_values(cuda_device, D, rise, size):
+    """Tiny values of V, then a token whose V is zero and whose score is above all others (by less than what moves the
+    reference): a zero step meets the largest power of two."""
+    rng = np.random.default_rng(D)
+    lens, ps = [70, 200], 16
+    bt, pages = make_table(rng, lens, ps)
+    k = (rng.standard_normal((pages, 1, ps, D)) * 0.01).astype(np.float32)
+    v = (rng.standard_normal((pages, 1, ps, D)) * size).astype(np.float32)
+    for b, t in ((0, 50), (1, 100), (1, 180)):
+        k[bt[b, t // ps], 0, t % ps] = rise / D
+        v[bt[b, t // ps], 0, t % ps] = 0.0
+    q = bf16(np.ones((2, 4, D)))
+    for workers in (0, 1):
+        attend(cuda_device, q, k, v, bt, lens, 1.0, workers)
