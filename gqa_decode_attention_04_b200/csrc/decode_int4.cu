@@ -17,10 +17,11 @@
 // lies below 2^-126, which is 2^-126 scale log2(e) 2^(24 - e) < 2^-15 of a score while |scale q| < 2^100.
 //   The minima's part of a score is one more MMA of depth 4 per tile, in tf32: m is exact there, and
 // sum(q_g) goes in as two parts of 11 bits.
-//   p s is rounded to fp16.  Steps may be of any size, so each row carries a power of two F that
-// keeps p s F below 2^15 (F is 2^115 at most, so steps below 2^-112 lose bits: 2^-25 / F = 2^-140 absolutely for
-// each token's weight); it moves with the running maximum, which itself moves only when a score
-// passes it by 2^12.  Scores, sums and outputs are fp32.
+//   p s is rounded to fp16.  Steps may be of any size, so each row carries a power of two F for each group of V
+// that keeps p s F below 2^15 (F is 2^115 at most, so steps below 2^-112 lose bits: 2^-25 / F = 2^-140 absolutely for
+// each token's weight); they move with the running maximum, which itself moves only when a score
+// passes it by 2^12.  (One F for both groups of a row would leave a group that is 2^-18 of the other, or less
+// beside one token of great weight, in fp16's subnormals.)  Scores, sums and outputs are fp32.
 //
 // Bound: HBM at small groups on paper -- 9/8 D bytes per token and kv head -- but in fact the
 // instructions that turn codes into MMA operands, whatever the number of query rows: about 320 per
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
         for (int c = 0; c < 2; ++c) h[nt][c] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * c);
       }
 
-      float o[G * 4][NT][4], l[NT][2], pm[NT][G][2], ref[NT][2], F[NT][2];
+      float o[G * 4][NT][4], l[NT][2], pm[NT][G][2], ref[NT][2], F[NT][G][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -441,9 +442,11 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
         for (int c = 0; c < 2; ++c) {
           l[nt][c] = 0.0f;
           ref[nt][c] = kNone;
-          F[nt][c] = 1.0f;
 #pragma unroll
-          for (int u = 0; u < G; ++u) pm[nt][u][c] = 0.0f;
+          for (int u = 0; u < G; ++u) {
+            pm[nt][u][c] = 0.0f;
+            F[nt][u][c] = 1.0f;
+          }
         }
       }
 
@@ -548,14 +551,15 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
                 pr[nt][2 * r + c] = ptx::ex2(y[c]);
                 if (ENDS && !seen[nt][2 * r + c]) pr[nt][2 * r + c] = 0.0f;
               }
-              ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(pr[nt][2 * r], pr[nt][2 * r + 1]), ptx::f2_pack(F[nt][0], F[nt][1])), y[0], y[1]);
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
+              for (int u = 0; u < G; ++u) {
+                ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(pr[nt][2 * r], pr[nt][2 * r + 1]), ptx::f2_pack(F[nt][u][0], F[nt][u][1])), y[0], y[1]);
 #pragma unroll
-                for (int u = 0; u < G; ++u) {
+                for (int c = 0; c < 2; ++c) {
                   w[nt][u][2 * r + c] = y[c] * step[r][u];
                   if (ENDS && !seen[nt][2 * r + c]) w[nt][u][2 * r + c] = 0.0f;
                 }
+              }
             }
             top = ptx::max3(top, pr[nt][0], pr[nt][1]);
             top = ptx::max3(top, pr[nt][2], pr[nt][3]);
@@ -581,25 +585,25 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
               const float a = ptx::ex2(ref[nt][c] - top);
               ref[nt][c] = top;
               l[nt][c] *= a;
-              float big = 0.0f;
 #pragma unroll
               for (int u = 0; u < G; ++u) {
                 pm[nt][u][c] *= a;
+                float big = 0.0f;
                 if (seen[nt][c]) big = fmaxf(big, ptx::ex2(at0 - top) * step[0][u]);
                 if (seen[nt][c + 2]) big = fmaxf(big, ptx::ex2(at1 - top) * step[1][u]);
-              }
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-              // the largest weight so far in [2^2, 2^3): 2^12 below the bound, as far as scores may pass
-              // the reference, and 2^16 above fp16's subnormals
-              const float before = a / F[nt][c];
-              const float f = inverse_pow2(fmaxf(big * 0x1p-2f, before));
-              const float scale = before * f;
-              F[nt][c] = f;
+                for (int d = 4; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+                // the largest weight so far in [2^2, 2^3): 2^12 below the bound, as far as scores may pass
+                // the reference, and 2^16 above fp16's subnormals
+                const float before = a / F[nt][u][c];
+                const float f = inverse_pow2(fmaxf(big * 0x1p-2f, before));
+                const float scale = before * f;
+                F[nt][u][c] = f;
 #pragma unroll
-              for (int m = 0; m < 4 * G; ++m) {
-                o[m][nt][c] *= scale;
-                o[m][nt][c + 2] *= scale;
+                for (int m = 0; m < 4; ++m) {
+                  o[4 * u + m][nt][c] *= scale;
+                  o[4 * u + m][nt][c + 2] *= scale;
+                }
               }
             }
           weigh();
@@ -709,7 +713,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
 #pragma unroll
           for (int u = 0; u < G; ++u) {
             // 1 / F: a power of two in [2^-115, 2^126], so it does not take the codes' 2^24 as well
-            const float over = __uint_as_float((254u << 23) - __float_as_uint(F[nt][c]));
+            const float over = __uint_as_float((254u << 23) - __float_as_uint(F[nt][u][c]));
             float y[8];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {

@@ -105,3 +105,22 @@ def test_a_row_of_zeros_behind_tiny_values(cuda_device, D, rise, size):
     q = bf16(np.ones((2, 4, D)))
     for workers in (0, 1):
         attend(cuda_device, q, k, v, bt, lens, 1.0, workers)
+
+
+@pytest.mark.parametrize("heads", [(4, 1), (16, 1)], ids=str)
+@pytest.mark.parametrize("above", [0.0, 3.0, 8.0])
+@pytest.mark.parametrize("ratio", [1e-3, 1e-5, 1e-7, 1e-8, 1e-20])
+def test_steps_of_the_groups_of_a_row(cuda_device, ratio, above, heads):
+    """One group of V smaller than the other by `ratio`; flat scores, or one token e^above above the others."""
+    rng = np.random.default_rng(int(above) + heads[0])
+    lens, ps, D = [1000, 37], 16, 128
+    bt, pages = make_table(rng, lens, ps)
+    for small in (0, 1):
+        k = (rng.standard_normal((pages, 1, ps, D)) * 0.01).astype(np.float32)
+        v = (rng.standard_normal((pages, 1, ps, D)) + 0.5).astype(np.float32)
+        v[..., 64 * small:64 * small + 64] *= np.float32(ratio)
+        for b, t in ((0, 5 if small else 900), (1, 20)):
+            k[bt[b, t // ps], 0, t % ps] = above / D
+        q = bf16(np.ones((2, heads[0], D)) + 0.01 * rng.standard_normal((2, heads[0], D)))
+        for workers in (0, 1):
+            attend(cuda_device, q, k, v, bt, lens, 1.0, workers)
