@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t excl[32 * kWarps];  // cost of the sequences before each thread's chunk
   __shared__ int64_t scan[kWarps];
+  __shared__ int longest[kWarps];
   __shared__ __align__(8) uint64_t full[kWarps][C::kStages];
   __shared__ Piece pieces[2 * kWarps];
   __shared__ Split kept;  // for the merges: the loop has no registers for it
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
 
   if (lane == 0) {
 #pragma unroll
-    for (int s = 0; s < C::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&full[warp][s]), 2);  // lanes 0 and 1
+    for (int s = 0; s < C::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&full[warp][s]), 2);  // the lanes of a unit's two tiles
     ptx::fence_mbarrier_init();
     pieces[2 * warp].units = 0;
     pieces[2 * warp + 1].units = 0;
@@ -205,15 +206,24 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   const int chunk = (p.num_seqs + 32 * kWarps - 1) / (32 * kWarps);
   {
     int64_t mine = 0;
+    int most = 0;
     const int b0 = threadIdx.x * chunk, b1 = min(p.num_seqs, b0 + chunk);
-    for (int b = b0; b < b1; ++b) mine += cost_of(checked_len(p, b));
+    for (int b = b0; b < b1; ++b) {
+      const int cost = cost_of(checked_len(p, b));
+      mine += cost;
+      most = max(most, cost);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += o;
     }
-    if (lane == 31) scan[warp] = incl;
+    if (lane == 31) {
+      scan[warp] = incl;
+      longest[warp] = most;
+    }
     __syncthreads();
     int64_t before = 0;
     for (int w = 0; w < warp; ++w) before += scan[w];
@@ -223,15 +233,20 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
   Split split;
   {
     int64_t total = 0;
-    for (int w = 0; w < kWarps; ++w) total += scan[w];
+    int most = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      total += scan[w];
+      most = max(most, longest[w]);
+    }
     split.total = total * segs;
     // Least work of a warp.  Few long segments are not cut into more than is merged in the time that it
     // saves: a unit takes 0.8 us, a warp merges eight CTAs' parts of a segment in 1 us, and n units a
-    // segment in ranges of x make n / 8 x parts: x = sqrt(n / 52).  (One sequence of 131072 tokens and one
+    // segment in ranges of x make n / 8 x parts: x = sqrt(n / 52).  The longest segment's n, since segments
+    // are merged side by side; sequences without tokens do not count.  (One sequence of 131072 tokens and one
     // kv head: 27 us, and 63 cut as finely as there are warps; three of 30000 19 and 32.)  A batch of a few
     // units is not cut finer than a segment of one: two sequences of 17 and 40 tokens take 6.2 us whole
     // and 7.9 cut.
-    int64_t least = static_cast<int64_t>(sqrtf(__fdividef(static_cast<float>(split.total), 52.0f * segs * p.num_seqs)));
+    int64_t least = static_cast<int64_t>(sqrtf(static_cast<float>(most) * (1.0f / 52.0f)));
     least = max(least, split.total <= 4 * kWarps ? int64_t{kSegCost + 1} : int64_t{1});
     split.workers = min(static_cast<int64_t>(gridDim.x) * kWarps, quotient(split.total + least - 1, least));
     split.per = split.total == 0 ? 0 : quotient(split.total, split.workers);
