@@ -227,12 +227,15 @@ cudaError_t launch_rows(RopeAppendParams p, int sms, cudaStream_t stream) {
   // 3.7 and 3.1, 600 6.3 and 4.4; 12 + 2 heads of 64: 400 tokens 2.5 and 3.5, 800 3.9 and 3.6.)
   const int64_t per_gpu = int64_t{kThreads * kBlocks} * sms / (D / 8);
   int64_t blocks;
-  const bool many = rows > 1 && p.num_tokens * static_cast<int64_t>(rows) > per_gpu;
+  const bool many = p.num_tokens * static_cast<int64_t>(rows) > per_gpu;
   if (many) {
     // Twice kBatch rows a thread while that leaves the GPU half full of threads: 16384 tokens of 32 + 8
-    // heads into bf16 71 us, and 77 with kBatch; 5987 of 12 + 2 heads of 64 into e4m3 8.1, and 6.4.
+    // heads into bf16 71 us, and 77 with kBatch; 5987 of 12 + 2 heads of 64 into e4m3 8.1, and 6.4.  The k and v
+    // rows count where they are more than q's, or are all there is: 593 sequences of 8 kv heads into 4 bits
+    // without rotation 4.6 us, and 23 with all 16 rows a thread (592, one row a thread: 3.3).
     p.spread_log2 = 0;
-    auto can = [&](int rows) { return (2 << p.spread_log2) <= kSlots && (2 << p.spread_log2) * rows <= p.num_heads; };
+    const int most = p.num_heads > 2 * p.num_kv_heads ? p.num_heads : 2 * p.num_kv_heads;
+    auto can = [&](int rows) { return (2 << p.spread_log2) <= kSlots && (2 << p.spread_log2) * rows <= most; };
     while (can(2 * kBatch)) ++p.spread_log2;
     if (static_cast<int64_t>(p.num_tokens) * (D / 8 << p.spread_log2) < int64_t{kThreads * kBlocks / 2} * sms)
       while (can(kBatch)) ++p.spread_log2;

@@ -158,3 +158,39 @@ def test_special_rows(cuda_device):
     for i in range(2):
         write_rows(want, t // 16, t % 16, i, x[i].float().numpy())
     assert np.array_equal(pool.cpu().numpy(), want)
+
+
+def microseconds(call, n=20):
+    """Device time of a call in a replayed graph (median of nine)."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            call()
+    times = []
+    for i in range(12):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3 / n)
+    return sorted(times[3:])[4]
+
+
+@pytest.mark.parametrize("Hk", [8, 32])
+def test_one_more_sequence_is_no_cliff(cuda_device, Hk):
+    """The first batch whose rows no longer fit one a thread takes about the time of the last that does (1.4 times;
+    7 to 13 where each thread took all rows of a token)."""
+    D = 128
+    fits = 1024 * torch.cuda.get_device_properties(0).multi_processor_count // (D // 8) // (2 * Hk)
+    took = []
+    for B in (fits, fits + 1):
+        x = torch.randn(2, B, Hk, D, device=cuda_device).bfloat16()
+        pool = torch.zeros(B // 16 + 1, Hk, 1, 18 * D, dtype=torch.uint8, device=cuda_device)
+        row = torch.arange(B, dtype=torch.int32, device=cuda_device)
+        table, pos = (row // 16)[:, None].contiguous(), row % 16
+        took.append(microseconds(lambda: gq.kv_append_int4(x[0], x[1], pool, table, pos)))
+    gq.check_device_error()
+    assert took[1] < 2.5 * took[0], took
