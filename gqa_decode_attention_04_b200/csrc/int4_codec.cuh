@@ -56,7 +56,8 @@ __device__ __forceinline__ float bf16_round(float x) {
 
 // Codes of this lane's 8 W channels (nibble n of words[w] = channel 8 w + n) of a group held by
 // 8 / W aligned lanes; pair = step (low half) | low (high half), the same in those lanes.  Every
-// lane of the warp takes part.
+// lane of the warp takes part; a group whose lanes have `wanted` false gets no codes, and has no say in how
+// the others' are found.
 //
 // Both quotients, range / 15 and (x - low) / step, are the correctly rounded ones: with r = RN(1 / d),
 // y = RN(a r) and the exact residual e = a - y d (one fma), RN(y + e r) is RN(a / d) (Markstein,
@@ -66,7 +67,7 @@ __device__ __forceinline__ float bf16_round(float x) {
 // bounds the writers (a pool of 150 MB: 28 us for its bytes), so it goes in packed pairs, and the
 // codes are put together as one exact number, c0 + 16 c1 + 256 c2 + 4096 c3.
 template <int W>
-__device__ __forceinline__ void quantize(const float (&x)[8 * W], uint32_t (&words)[W], uint32_t& pair) {
+__device__ __forceinline__ void quantize(const float (&x)[8 * W], uint32_t (&words)[W], uint32_t& pair, bool wanted = true) {
   float lo = x[0], hi = x[0];
 #pragma unroll
   for (int i = 1; i < 8 * W; ++i) {
@@ -81,7 +82,7 @@ __device__ __forceinline__ void quantize(const float (&x)[8 * W], uint32_t (&wor
   const float low = bf16_round(lo);
   const float range = __fsub_rn(hi, lo);
   const bool usual = range >= 0x1p-60f && range <= 0x1p60f && fabsf(low) < INFINITY;
-  if (__all_sync(0xffffffffu, usual)) {
+  if (__all_sync(0xffffffffu, usual || !wanted)) {
     constexpr float kFifteenth = 1.0f / 15.0f;
     float step = __fmul_rn(range, kFifteenth);
     step = bf16_round(__fmaf_rn(__fmaf_rn(-step, 15.0f, range), kFifteenth, step));

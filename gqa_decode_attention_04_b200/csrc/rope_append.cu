@@ -183,9 +183,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
 #pragma unroll
       for (int m = 0; m < 8; ++m) x[m] = is_v ? x[m] : turned[m];
     }
+    const bool wanted = live && r >= 0 && r < cached;
     uint32_t pair = 0, word[1] = {0};
-    if (CACHE == kCacheInt4) int4::quantize<1>(x, word, pair);  // (by the whole warp: it shuffles)
-    if (live && r >= 0 && r < cached) {
+    if (CACHE == kCacheInt4) int4::quantize<1>(x, word, pair, wanted);  // (by the whole warp: it shuffles)
+    if (wanted) {
       const int h = r - (is_v ? p.num_kv_heads : 0);
       const int64_t page_head = static_cast<int64_t>(page) * p.num_kv_heads + h;
       if (CACHE == kCacheInt4) {
