@@ -68,7 +68,17 @@ def build_fastcall(verbose: bool = False, force: bool = False) -> str:
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
-    build_fastcall(verbose, force)
+    """The library, then the marshalling module, which it does not need: without a C++ compiler or the headers of
+    Python or torch the calls go through ctypes."""
+    build_library(verbose, force)
+    try:
+        build_fastcall(verbose, force)
+    except (RuntimeError, OSError) as e:
+        sys.stderr.write(f"{e}: built without the marshalling module\n")
+    return LIB
+
+
+def build_library(verbose: bool = False, force: bool = False) -> str:
     if not force and not needs_rebuild():
         return LIB
     objdir = os.path.join(HERE, "_build")
