@@ -14,6 +14,7 @@ is missing or the tensors are not on a CUDA device, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -122,12 +123,15 @@ _entry = {}        # addresses of the entry points that it calls
 
 
 def _load_fast(lib) -> None:
-    """Loads the in-tree marshalling module.  (Without it, as in a tree where only the library was built,
-    the same calls go through ctypes.)"""
+    """Loads the in-tree marshalling module.  (Without it, as in a tree where only the library was built, or one
+    built for another Python, torch or source, the same calls go through ctypes.)"""
     global _fast
+    from .build import fastcall_path
     try:
-        from . import _fastcall
-    except ImportError:
+        spec = importlib.util.spec_from_file_location(__name__ + "._fastcall", fastcall_path())
+        _fastcall = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_fastcall)
+    except (ImportError, OSError):
         return
     for name in ("gqa_rope_kv_append", "gqa_rope_kv_append_fp8", "gqa_rope_kv_append_int4", "gqa_kv_quantize_int4",
                  "gqa_kv_dequantize_int4", "gqa_paged_decode_attn_int4", "gqa_paged_multi_query_attn_int4",

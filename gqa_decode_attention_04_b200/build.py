@@ -1,5 +1,5 @@
 """Build the CUDA library in-tree: csrc/*.cu (+ host-only csrc/*.cpp) -> libgqa_decode.so
-(sm_100a only), and the binding's marshalling module csrc/fastcall.cc -> _fastcall.so.
+(sm_100a only), and the binding's marshalling module csrc/fastcall.cc -> _fastcall.<key>.so.
 
 Usage:  python -m gqa_decode_attention_04_b200.build [--verbose]
 The shared object is written next to this file so it travels with the source tree.
@@ -7,6 +7,7 @@ The shared object is written next to this file so it travels with the source tre
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import subprocess
 import sys
@@ -18,7 +19,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgqa_decode.so")
 FAST_SOURCE = os.path.join(CSRC, "fastcall.cc")
-FAST = os.path.join(HERE, "_fastcall.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -46,16 +46,28 @@ def needs_rebuild() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def fastcall_path() -> str:
+    """Where the marshalling module for this Python, this torch and these sources is.  The name says what it was
+    built for, so one that was built for others is never loaded, and is not there when asked for."""
+    import torch
+    key = hashlib.sha256(repr((sys.version_info[:3], sysconfig.get_config_var("SOABI"), torch.__version__)).encode())
+    for path in [FAST_SOURCE, *sorted(glob.glob(os.path.join(INCLUDE, "*.h")))]:
+        with open(path, "rb") as f:
+            key.update(f.read())
+    return os.path.join(HERE, f"_fastcall.{key.hexdigest()[:16]}.so")
+
+
 def build_fastcall(verbose: bool = False, force: bool = False) -> str:
     """The extension module that checks and passes torch tensors (host code only)."""
-    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= os.path.getmtime(FAST_SOURCE):
-        return FAST
+    fast = fastcall_path()
+    if not force and os.path.exists(fast):
+        return fast
     import torch
     root = os.path.dirname(torch.__file__)
     lib = os.path.join(root, "lib")
-    tmp = FAST + ".tmp"
+    tmp = fast + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-shared", "-fPIC", "-std=c++17",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            "-isystem", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"], FAST_SOURCE, "-o", tmp,
            "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -63,8 +75,10 @@ def build_fastcall(verbose: bool = False, force: bool = False) -> str:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {FAST_SOURCE}")
-    os.replace(tmp, FAST)
-    return FAST
+    for old in glob.glob(os.path.join(HERE, "_fastcall*.so")):
+        os.remove(old)
+    os.replace(tmp, fast)
+    return fast
 
 
 def build(verbose: bool = False, force: bool = False) -> str:

@@ -1,9 +1,11 @@
-"""CPU: the build makes the library whatever becomes of the marshalling module."""
+"""CPU: the build makes the library whatever becomes of the marshalling module, and the module that is loaded is one
+that was built for this Python, this torch and these sources."""
 import os
 import subprocess
 
 import pytest
 
+import gqa_decode_attention_04_b200 as gq
 from gqa_decode_attention_04_b200 import build as B
 
 
@@ -14,7 +16,6 @@ def tree(tmp_path, monkeypatch):
     state = {"commands": [], "broken": False}
     monkeypatch.setattr(B, "HERE", str(tmp_path))
     monkeypatch.setattr(B, "LIB", str(tmp_path / "libgqa_decode.so"))
-    monkeypatch.setattr(B, "FAST", str(tmp_path / "_fastcall.so"))
     monkeypatch.setenv("CXX", "some-g++")
 
     def run(cmd, **kw):
@@ -44,3 +45,42 @@ def test_a_library_that_fails_is_an_error(tree, monkeypatch):
     monkeypatch.setattr(subprocess, "run", fails)
     with pytest.raises(RuntimeError, match="nvcc"):
         B.build(force=True)
+
+
+def modules():
+    return sorted(n for n in os.listdir(B.HERE) if n.startswith("_fastcall"))
+
+
+def test_the_module_is_rebuilt_for_another_torch_python_or_source(tree, monkeypatch, tmp_path):
+    import torch
+    B.build()
+    (first,) = modules()
+    n = len(tree["commands"])
+    B.build_fastcall()
+    assert len(tree["commands"]) == n  # nothing to do
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    B.build_fastcall()
+    (second,) = modules()
+    monkeypatch.setattr(B.sysconfig, "get_config_var", lambda name: "other")
+    B.build_fastcall()
+    (third,) = modules()
+    header = tmp_path / "include"
+    header.mkdir()
+    (header / "gqa_int4.h").write_text("another argument\n")
+    monkeypatch.setattr(B, "INCLUDE", str(header))
+    B.build_fastcall()
+    (fourth,) = modules()
+    assert len({first, second, third, fourth}) == 4
+    assert len(tree["commands"]) == n + 3
+
+
+def test_a_module_built_for_others_is_not_loaded(monkeypatch):
+    lib = gq.load_library()
+    monkeypatch.setattr(gq, "_fast", None)
+    gq._load_fast(lib)
+    assert gq._fast is not None
+    import torch
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    monkeypatch.setattr(gq, "_fast", None)
+    gq._load_fast(lib)
+    assert gq._fast is None
