@@ -10,6 +10,9 @@
 #include <climits>
 #include <cmath>
 
+#include "gqa_int4.h"
+#include "gqa_rope.h"
+
 namespace {
 
 // o as a contiguous CUDA tensor of this type on device dev, else nullptr.
@@ -32,6 +35,12 @@ int64_t row_stride(const at::Tensor& t) {
 }
 
 void* address(PyObject* o) { return PyLong_AsVoidPtr(o); }
+
+// The entry point at an address, with the type that its header gives it.
+#define ENTRY(name, o) reinterpret_cast<decltype(&name)>(address(o))
+
+const int32_t* ints(const at::Tensor* t) { return static_cast<const int32_t*>(t->data_ptr()); }
+const float* floats(const at::Tensor* t) { return static_cast<const float*>(t->data_ptr()); }
 
 constexpr auto kBf16 = c10::ScalarType::BFloat16;
 constexpr auto kByte = c10::ScalarType::Byte;
@@ -61,16 +70,12 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const size_t bytes = static_cast<size_t>(ws->numel());
   int status;
   if (dims == 3) {
-    using Fn = int (*)(const void*, const void*, const void*, const void*, void*, int, int, int, int, int, float, int, int, void*,
-                       size_t, void*);
-    status = reinterpret_cast<Fn>(address(a[0]))(q->data_ptr(), pool->data_ptr(), bt->data_ptr(), sl->data_ptr(), out->data_ptr(), B,
-                                                 H, Hk, D, ps, static_cast<float>(scale), mb, P, ws->data_ptr(), bytes, stream);
+    status = ENTRY(gqa_paged_decode_attn_int4, a[0])(q->data_ptr(), pool->data_ptr(), ints(bt), ints(sl), out->data_ptr(), B, H, Hk, D,
+                                                     ps, static_cast<float>(scale), mb, P, ws->data_ptr(), bytes, stream);
   } else {
-    using Fn = int (*)(const void*, const void*, const void*, const void*, void*, int, int, int, int, int, int, float, int, int,
-                       void*, size_t, void*);
-    status = reinterpret_cast<Fn>(address(a[0]))(q->data_ptr(), pool->data_ptr(), bt->data_ptr(), sl->data_ptr(), out->data_ptr(), B,
-                                                 static_cast<int>(q->size(1)), H, Hk, D, ps, static_cast<float>(scale), mb, P,
-                                                 ws->data_ptr(), bytes, stream);
+    status = ENTRY(gqa_paged_multi_query_attn_int4, a[0])(q->data_ptr(), pool->data_ptr(), ints(bt), ints(sl), out->data_ptr(), B,
+                                                          static_cast<int>(q->size(1)), H, Hk, D, ps, static_cast<float>(scale), mb, P,
+                                                          ws->data_ptr(), bytes, stream);
   }
   return PyLong_FromLong(status);
 }
@@ -84,11 +89,10 @@ PyObject* convert(PyObject*, PyObject* const* a, Py_ssize_t n) {
   WANT(k && v && pool && v->sizes() == k->sizes());
   const int64_t P = k->size(0), Hk = k->size(1), ps = k->size(2), d = k->size(3);
   WANT(ps % 16 == 0 && d <= 1024 && pool->size(0) == P && pool->size(1) == Hk && pool->size(2) == ps / 16 && pool->size(3) == 18 * d);
-  using Fn = int (*)(const void*, const void*, const void*, int, int, int, int, void*);
   void *x = k->data_ptr(), *y = v->data_ptr(), *z = pool->data_ptr();
-  const Fn fn = reinterpret_cast<Fn>(address(a[0]));
   const int p = static_cast<int>(P), h = static_cast<int>(Hk), s = static_cast<int>(ps), dd = static_cast<int>(d);
-  return PyLong_FromLong(back ? fn(z, x, y, p, h, s, dd, address(a[2])) : fn(x, y, z, p, h, s, dd, address(a[2])));
+  return PyLong_FromLong(back ? ENTRY(gqa_kv_dequantize_int4, a[0])(z, x, y, p, h, s, dd, address(a[2]))
+                              : ENTRY(gqa_kv_quantize_int4, a[0])(x, y, z, p, h, s, dd, address(a[2])));
 }
 
 // rope(fn, device, stream, q, k_new, v_new, cos_sin, q_out, block_table, positions, seq_ids or None,
@@ -130,26 +134,20 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int t = static_cast<int>(T), seqs = static_cast<int>(bt->size(0)), h = static_cast<int>(H), hk = static_cast<int>(Hk),
             dd = static_cast<int>(d), r = static_cast<int>(cs->size(1)), mp = static_cast<int>(cs->size(0)),
             page = static_cast<int>(ps), mb = static_cast<int>(bt->size(1)), P = static_cast<int>(pool[0]->size(0));
-  const void *qp = q->data_ptr(), *kp = k->data_ptr(), *vp = v->data_ptr(), *cp = cs->data_ptr(), *tp = bt->data_ptr(),
-             *pp = pos->data_ptr(), *ip = ids ? ids->data_ptr() : nullptr;
-  void *op = qo->data_ptr(), *fn = address(a[0]), *p0 = pool[0]->data_ptr();
+  const void *qp = q->data_ptr(), *kp = k->data_ptr(), *vp = v->data_ptr();
+  const float* cp = floats(cs);
+  const int32_t *tp = ints(bt), *pp = ints(pos), *ip = ids ? ints(ids) : nullptr;
+  void *op = qo->data_ptr(), *p0 = pool[0]->data_ptr();
   int status;
   if (n == 13) {
-    using Fn = int (*)(const void*, const void*, const void*, const void*, void*, void*, const void*, const void*, const void*, int,
-                       int, int, int, int, int, int, int, int64_t, int64_t, int64_t, int, int, int, void*);
-    status = reinterpret_cast<Fn>(fn)(qp, kp, vp, cp, op, p0, tp, pp, ip, t, seqs, h, hk, dd, r, inter, mp, qs, ks, vs, page, mb, P,
-                                      stream);
+    status = ENTRY(gqa_rope_kv_append_int4, a[0])(qp, kp, vp, cp, op, p0, tp, pp, ip, t, seqs, h, hk, dd, r, inter, mp, qs, ks, vs, page,
+                                                  mb, P, stream);
   } else if (n == 14) {
-    using Fn = int (*)(const void*, const void*, const void*, const void*, void*, void*, void*, const void*, const void*, const void*,
-                       int, int, int, int, int, int, int, int, int64_t, int64_t, int64_t, int, int, int, void*);
-    status = reinterpret_cast<Fn>(fn)(qp, kp, vp, cp, op, p0, pool[1]->data_ptr(), tp, pp, ip, t, seqs, h, hk, dd, r, inter, mp, qs,
-                                      ks, vs, page, mb, P, stream);
+    status = ENTRY(gqa_rope_kv_append, a[0])(qp, kp, vp, cp, op, p0, pool[1]->data_ptr(), tp, pp, ip, t, seqs, h, hk, dd, r, inter, mp,
+                                             qs, ks, vs, page, mb, P, stream);
   } else {
-    using Fn = int (*)(const void*, const void*, const void*, const void*, void*, void*, void*, const void*, const void*, const void*,
-                       const void*, const void*, int, int, int, int, int, int, int, int, int64_t, int64_t, int64_t, int, int, int,
-                       void*);
-    status = reinterpret_cast<Fn>(fn)(qp, kp, vp, cp, op, p0, pool[1]->data_ptr(), pool[2]->data_ptr(), pool[3]->data_ptr(), tp, pp,
-                                      ip, t, seqs, h, hk, dd, r, inter, mp, qs, ks, vs, page, mb, P, stream);
+    status = ENTRY(gqa_rope_kv_append_fp8, a[0])(qp, kp, vp, cp, op, p0, pool[1]->data_ptr(), floats(pool[2]), floats(pool[3]), tp, pp,
+                                                 ip, t, seqs, h, hk, dd, r, inter, mp, qs, ks, vs, page, mb, P, stream);
   }
   return PyLong_FromLong(status);
 }
@@ -179,11 +177,9 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
        v->sizes() == k->sizes() && bt->size(0) == seqs && pos->size(0) == seqs && sl->size(0) == seqs && out->sizes() == q->sizes());
   const double scale = a[14] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : PyFloat_AsDouble(a[14]);
   if (PyErr_Occurred()) return nullptr;
-  using Fn = int (*)(const void*, const void*, const void*, const void*, void*, void*, const void*, const void*, const void*, void*, int,
-                     int, int, int, int, int, int, int, float, int, int, void*, size_t, void*);
-  const int status = reinterpret_cast<Fn>(address(a[0]))(
-      q->data_ptr(), k->data_ptr(), v->data_ptr(), cs ? cs->data_ptr() : nullptr, qr ? qr->data_ptr() : nullptr, pool->data_ptr(),
-      bt->data_ptr(), pos->data_ptr(), sl->data_ptr(), out->data_ptr(), static_cast<int>(seqs), static_cast<int>(q->size(1)),
+  const int status = ENTRY(gqa_decode_step_int4, a[0])(
+      q->data_ptr(), k->data_ptr(), v->data_ptr(), cs ? floats(cs) : nullptr, qr ? qr->data_ptr() : nullptr, pool->data_ptr(),
+      ints(bt), ints(pos), ints(sl), out->data_ptr(), static_cast<int>(seqs), static_cast<int>(q->size(1)),
       static_cast<int>(Hk), static_cast<int>(d), cs ? static_cast<int>(cs->size(1)) : 0, inter, cs ? static_cast<int>(cs->size(0)) : 0,
       static_cast<int>(16 * pool->size(2)), static_cast<float>(scale), static_cast<int>(bt->size(1)),
       static_cast<int>(pool->size(0)), ws->data_ptr(), static_cast<size_t>(ws->numel()), stream);

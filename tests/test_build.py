@@ -84,3 +84,13 @@ def test_a_module_built_for_others_is_not_loaded(monkeypatch):
     monkeypatch.setattr(gq, "_fast", None)
     gq._load_fast(lib)
     assert gq._fast is None
+
+
+def test_the_module_takes_its_entry_points_types_from_the_headers():
+    """A call whose arguments no longer are the entry point's does not compile."""
+    with open(B.FAST_SOURCE) as f:
+        text = f.read()
+    assert "(*)(" not in text.replace("reinterpret_cast<void (*)()>", "")
+    for name in ("gqa_rope_kv_append", "gqa_rope_kv_append_fp8", "gqa_rope_kv_append_int4", "gqa_kv_quantize_int4",
+                 "gqa_kv_dequantize_int4", "gqa_paged_decode_attn_int4", "gqa_paged_multi_query_attn_int4", "gqa_decode_step_int4"):
+        assert f"ENTRY({name}," in text
