@@ -24,12 +24,12 @@
 // beside one token of great weight, in fp16's subnormals.)  Scores, sums and outputs are fp32.
 //
 // Bound: HBM at small groups on paper -- 9/8 D bytes per token and kv head -- but in fact the
-// instructions that turn codes into MMA operands, whatever the number of query rows: about 320 per
-// tile of 16 tokens and row tile, two thirds of them on the integer pipe at half rate.  4 sequences of
-// 131072 tokens, 8 kv heads, 8 rows each: 127 us (4.7 TB/s, 72 % of a copy's rate), 107 with the copies
-// alone.  256 sequences of 1 to 32768 tokens: 176 us (5.3 TB/s, 81 %).  More rows
-// widen each tile again for every 16: 96 rows (64 sequences of 8192 tokens, one kv head) 146 us, 0.18
-// PFLOP/s.
+// instructions that turn codes into MMA operands, whatever the number of query rows: about 315 per
+// tile of 16 tokens and row tile, about half of them on the integer pipe at half rate, issued at 0.55 a cycle:
+// what a warp waits for most is the latency of the one before.  4 sequences of 131072 tokens, 8 kv heads, 8 rows
+// each: 130 us (4.6 TB/s, 71 % of a copy's rate), 107 with the copies alone.  256 sequences of 1 to 32768 tokens:
+// 180 us (5.2 TB/s, 79 %).  More rows widen each tile again for every 16: 96 rows (64 sequences of 8192
+// tokens, one kv head) 144 us, 0.18 PFLOP/s.  (Times here are of calls replayed in a graph.)
 //
 // Work.  The list of units (sequence, kv head, row tile, 32 tokens), in that order, is cut into one
 // contiguous range of equal cost per WARP.  Each warp streams its range through its own ring of
@@ -37,12 +37,12 @@
 // together), and keeps the running maximum, sum and output of its current segment in registers;
 // there is no producer warp and no barrier in the loop.  The copies' cursor runs kStages units ahead;
 // lane i holds the address of the i-th tile of a window of 32, so a unit costs no index arithmetic.
-// (One producer warp for the CTA instead, with registers moved to the others: 142 us for 135, and
-// 42 for 36 on 32 sequences of 512 to 4096 tokens.)  A segment wholly inside a warp's range is written
+// (One producer warp for the CTA instead, with registers moved to the others, against the kernel of its
+// time: 142 us for 135, and 42 for 36 on 32 sequences of 512 to 4096 tokens.)  A segment wholly inside a warp's range is written
 // out at once.  What a range cuts is left in shared memory or the workspace (at most the first and the
 // last segment of a warp), merged over the CTA's warps after one __syncthreads, and over CTAs through
 // two workspace slots per CTA: the warp that is last to arrive at the counter of a segment's two rows
-// merges those.  (With a barrier of the CTA and one counter a segment: 33.4 us for 31.8 on that batch.)
+// merges those.  (With a barrier of the CTA and one counter a segment, then: 33.4 us for 31.8 on that batch.)
 // Which order the CTAs arrive in changes nothing: the parts are summed in the order of the list.
 //
 // The S tile is computed transposed, S^T = K Q^T (tokens on the MMA's 16-row side, 8 query
@@ -67,9 +67,10 @@ static_assert((2 * kWarps & (2 * kWarps - 1)) == 0 && 2 * kWarps <= 32, "a lane 
 constexpr float kNone = -3.0e38f;   // reference of a row that has seen no token
 
 // Rows of a merge, and records whose rows are loaded at a time (what a merge waits for is the way to L2,
-// but each costs its instructions where there are fewer): 32 sequences of 512 to 4096 tokens take 31.7 us
-// with (2, 5), 31.6 with (2, 4), 31.7 with (2, 2), 33.0 with (1, 4); with four query tokens 47.7, 47.8, 46.6,
-// 52.7; 4 of 131072 127.4, 126.5, 128.7, 130.7; 64 of 8192 with 96 heads 146.4, 150, 149.7, 150.4.
+// but each costs its instructions where there are fewer): 32 sequences of 512 to 4096 tokens take 32.8 us
+// with (2, 5), 32.7 with (2, 4), 32.6 with (2, 2), 34.0 with (1, 4); with four query tokens 49.9, 49.6, 48.3,
+// 55.5; 4 of 131072 130.2, 130.5, 130.5, 134.3; 64 of 8192 with 96 heads 144.3, 144.1, 143.5, 152.9; one of 131072
+// beside 20 of 2000, one kv head, 30.2, 30.8, 34.8 with (2, 2).
 constexpr int kMergeRows = 2, kFlight = 5;
 
 template <int D, int NT>
@@ -102,8 +103,8 @@ constexpr int kUnit = 2 * int4::kTile;  // tokens per step of a warp
 
 // What a segment costs a warp beside its units, in units: fetching q, ending and leaving a piece.
 // The list is cut by it, since some warps get dozens of short sequences: 256 sequences of 1 to 32768
-// tokens took 266 us with 0, 208 with 1, 182 with 2, 183 with 4; a batch of 32 of 512 to 4096 tokens
-// 37.9, 36.6, 36.0, 36.1, and with four query tokens 61, 51.9, 50.6, 48.7.
+// tokens take 187 us with 2, 180 with 3, 181 with 4 (266 with 0 and 208 with 1 in an earlier state); a batch of 32
+// of 512 to 4096 tokens 33.5, 32.8, 32.8, and with four query tokens 50.1, 49.9, 47.1.
 constexpr int kSegCost = 3;
 
 __device__ __forceinline__ int units_of(int len) {
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(32 * kWarps, (Cfg<D, NT>::kCtas)) decode_int4_
     // saves: a unit takes 0.8 us, a warp merges eight CTAs' parts of a segment in 1 us, and n units a
     // segment in ranges of x make n / 8 x parts: x = sqrt(n / 52).  The longest segment's n, since segments
     // are merged side by side; sequences without tokens do not count.  (One sequence of 131072 tokens and one
-    // kv head: 27 us, and 63 cut as finely as there are warps; three of 30000 19 and 32.)  A batch of a few
+    // kv head: 29 us, and 57 cut as finely as there are warps; three of 30000 19 and 31.)  A batch of a few
     // units is not cut finer than a segment of one: two sequences of 17 and 40 tokens take 6.2 us whole
     // and 7.9 cut.
     int64_t least = static_cast<int64_t>(sqrtf(static_cast<float>(most) * (1.0f / 52.0f)));
@@ -958,8 +959,8 @@ cudaError_t launch(const Int4DecodeParams& p, int grid, cudaStream_t stream, boo
 
 // 8 rows per segment while a kv head has no more than that, else 16, which widen each tile once for both
 // halves but leave registers for half the warps: a kv head with 16 rows (32 sequences of 512 to 4096
-// tokens, four query tokens) takes 47 us with 16 and 61 with 8; one with 96 (64 of 8192 tokens) 146 and
-// 193 us, and 154 with 24 rows a segment, whose output no longer fits the registers.
+// tokens, four query tokens) takes 50 us with 16 and 55 with 8; one with 96 (64 of 8192 tokens) 144 and
+// 189 us, and 154 (then) with 24 rows a segment, whose output no longer fits the registers.
 Int4Plan plan_decode_int4(int head_dim, int rows) {
   if (head_dim == 64) return rows <= 8 ? plan_of<64, 1>() : plan_of<64, 2>();
   return rows <= 8 ? plan_of<128, 1>() : plan_of<128, 2>();

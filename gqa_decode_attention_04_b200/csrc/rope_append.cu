@@ -7,10 +7,10 @@
 // of a channel lies rotary_dim / 16 lanes away: the pair is brought together by shuffles of
 // the packed bf16 words, so no element is read twice.  A thread keeps its cos and sin for all
 // the rows it handles (the same channels of several heads of one token).
-//   Measured: one token of 32 + 8 heads 2.0 us and 256 of them into bf16 2.9 us (the launch, then two
-// dependent loads: position, then block table and angles); 5987 tokens of 12 + 2 heads of 64 into e4m3 5.6
-// us (4.2 TB/s), 16384 of 32 + 8 of 128 into bf16 70 us (5.8 TB/s, 89 % of a copy's rate), of 64 + 8 into 4
-// bits, the pool read back, 144 us (5.6 TB/s, 85 %).
+//   Measured: one token of 32 + 8 heads 2.0 us and 256 of them into bf16 2.8 us (the launch, then two
+// dependent loads: position, then block table and angles); 5987 tokens of 12 + 2 heads of 64 into e4m3 5.9
+// us (4.1 TB/s), 16384 of 32 + 8 of 128 into bf16 69 us (5.9 TB/s, 90 % of a copy's rate), of 64 + 8 into 4
+// bits, the pool read back, 146 us (5.5 TB/s, 84 %).
 #include <climits>
 
 #include <cuda_fp8.h>
@@ -42,8 +42,8 @@ __device__ __forceinline__ uint32_t codes2(float a, float b, float s) {
 // k and v rows.  Otherwise one row a thread, p.chunks blocks per token.
 template <int D, int CACHE, bool MANY, bool INTER>
 __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const RopeAppendParams p) {
-  // A decode launched right after this one may start its prologue; it waits for this grid
-  // before it reads anything that is written here.
+  // The attention of a 4-bit step, launched right after this one, may start its prologue; it waits for this grid
+  // before it reads anything that is written here.  (All other calls wait for the whole grid.)
   ptx::pdl_launch_dependents();
   constexpr int kLanes = D / 8;
   constexpr int kSlots = kThreads / kLanes;  // rows in flight in a block
