@@ -124,3 +124,20 @@ def test_steps_of_the_groups_of_a_row(cuda_device, ratio, above, heads):
         q = bf16(np.ones((2, heads[0], D)) + 0.01 * rng.standard_normal((2, heads[0], D)))
         for workers in (0, 1):
             attend(cuda_device, q, k, v, bt, lens, 1.0, workers)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_largest_values_of_v_under_rising_scores(cuda_device, D):
+    """The same sums where most weights are as far above the reference as they may be: e^8.3 = 2^11.97."""
+    rng = np.random.default_rng(D)
+    lens, ps = [32, 160], 16
+    bt, pages = make_table(rng, lens, ps)
+    k = (rng.standard_normal((pages, 1, ps, D)) * 0.001).astype(np.float32)
+    for b, n in enumerate(lens):
+        for t in range(16, n):
+            k[bt[b, t // ps], 0, t % ps] = 8.3 / D
+    v = rng.uniform(-1.0, 1.0, (pages, 1, ps, D)).astype(np.float32)
+    v[..., ::3] = np.abs(v[..., ::3]) * 0.25 + 0.75
+    q = bf16(np.ones((2, 4, D)))
+    for workers in (0, 1):
+        attend(cuda_device, q, k, v * np.float32(2.0 ** 115 / 160), bt, lens, 1.0, workers)
